@@ -77,7 +77,14 @@ typedef enum fcm_status {
  * weights, which holds up to C = 128); other INT8 requests return FCM_ERR_UNSUPPORTED.  The results are exact: the same integers on every run and in every
  * mode. */
 typedef enum fcm_dtype { FCM_F32 = 0, FCM_F16 = 1, FCM_BF16 = 2, FCM_I8 = 3 } fcm_dtype;
-typedef enum fcm_act { FCM_ACT_NONE = 0, FCM_ACT_RELU = 1, FCM_ACT_RELU6 = 2 } fcm_act;
+/* FCM_ACT_SILU, v / (1 + e^-v), is taken by the sequence layers at the end of this header; the
+ * fused modules refuse it. */
+typedef enum fcm_act {
+    FCM_ACT_NONE = 0,
+    FCM_ACT_RELU = 1,
+    FCM_ACT_RELU6 = 2,
+    FCM_ACT_SILU = 3
+} fcm_act;
 /* The module's layer pair.  DEPTHWISE and DENSE: a k x k first convolution, then 1x1.
  * POINTWISE (PWDW): a 1x1 first convolution C -> Cm (Cm = mid, or C when mid is 0), then a
  * depthwise k x k convolution over the Cm channels; k_out must equal Cm. */
@@ -337,6 +344,89 @@ typedef struct {
 FCM_API fcm_status fcm_fuse_plan(const fcm_layer *layers, int n_layers, int batch,
                                  int num_sms, long long l1_bytes, int elem_bytes,
                                  fcm_layer_plan *out, long long *total_gma);
+
+/* ---- Layers over sequences: a state space block's causal depthwise convolution and selective
+ * scan, and its pointwise layers for a few tokens with 4-bit weights.
+ *
+ * These calls keep no handle: weights are read where they lie, no workspace is needed, nothing
+ * is allocated.  Conventions beyond those at the top of this header:
+ *  - Every pointer but the descriptor is device memory owned by the caller, aligned to its
+ *    element (qw of fcm_w4_matvec: 16 bytes); the calls run on the current device, enqueue on
+ *    `stream` and return.  What the host cannot see (seq_start, slot) is bounded by the kernels
+ *    as said below: no value in them makes a kernel read or write outside the tensors described.
+ *  - Activations are rows of channels, one row per token, `ld_*` elements apart (0: the row's
+ *    own length, rows contiguous), so a layer reads and writes column blocks of wider tensors.
+ *    16-byte aligned pointers and row distances run fastest; any others are served.
+ *  - dtype is FCM_F32, FCM_F16 or FCM_BF16 (fcm_w4_matvec: the last two).  Products, sums,
+ *    states of the scan, exponentials and activations are float32; each output is rounded once.
+ *  - Outputs must not overlap inputs, except that state_out may be state_in itself.
+ *  - Kernels are launched with programmatic stream serialization allowed, as fcm_run's are.
+ *  - Results do not depend on the launch: the same bits on every run on the same device. */
+
+/* Which rows form which sequence, and where each sequence's state lies.
+ * Without seq_start every sequence has max_len rows and tokens = n_seq * max_len.  With it (int32
+ * [n_seq + 1], not decreasing) sequence q has rows seq_start[q] to seq_start[q+1]; max_len is an
+ * upper bound of their lengths, and rows past it or outside [0, tokens) are left alone.  A
+ * sequence may be empty: its state passes through.  Rows of no sequence are not written.
+ * slot (int32 [n_seq], optional) gives the row of each sequence in the state tensors, which have
+ * `slots` rows; without it sequence q uses row q.  A sequence whose slot is outside [0, slots)
+ * starts from zero and its state is not kept.  Two sequences must not share a slot. */
+typedef struct fcm_seqs {
+    long long tokens;      /* rows of the activations                                      */
+    int n_seq, max_len;    /* sequences, and the longest one's length (single tokens: 1)   */
+    int slots;             /* rows of the state tensors; >= n_seq without slot             */
+    const int *seq_start;  /* device, may be NULL                                          */
+    const int *slot;       /* device, may be NULL                                          */
+} fcm_seqs;
+
+/* Causal depthwise convolution: with xx = the sequence's ksize-1 cached rows, then its rows of x,
+ *     y[i,d] = act(s[d] * sum_j w[d,j] * xx[i+j,d] + b[d]).
+ * x [tokens][c], y [tokens][c], w [c][ksize] (storage dtype), s and b [c] float32 (NULL: 1, 0).
+ * state_in / state_out [slots][ksize-1][c] in the storage dtype hold the cached rows, oldest
+ * first; state_in NULL starts from zeros, state_out NULL keeps nothing.  ksize 1 to 8 (1: no
+ * state, and both state pointers are ignored). */
+typedef struct fcm_causal_conv_desc {
+    fcm_seqs seqs;
+    int c, ksize, dtype, act;
+    long long ld_x, ld_y;
+} fcm_causal_conv_desc;
+FCM_API fcm_status fcm_causal_conv(const fcm_causal_conv_desc *desc, const void *x, const void *w,
+                                   const float *s, const float *b, const void *state_in, void *y,
+                                   void *state_out, void *stream);
+
+/* Selective scan: per sequence, channel d of group g = d / (c / groups) and state n,
+ *     D       = softplus(dt[t,d] + dt_bias[d])              (softplus 0: dt[t,d] + dt_bias[d])
+ *     h[d,n]  = exp(D * a[d,n]) * h[d,n] + D * x[t,d] * bm[t,g,n]
+ *     y[t,d]  = (sum_n cm[t,g,n] * h[d,n] + skip[d] * x[t,d]) * silu(z[t,d])
+ * x, dt, z, y [tokens][c]; bm, cm [tokens][groups][n_state] with rows ld_b, ld_c apart; a
+ * [c][n_state], skip, dt_bias [c] float32.  skip, z, dt_bias may be NULL: the term, the gate and
+ * the bias are left out.  state_in / state_out [slots][c][n_state] float32 hold h before and
+ * after; state_in NULL starts from zeros, state_out NULL keeps nothing.  n_state 1 to 128;
+ * groups divides c.  Any dt and a are taken; a state grows where D * a > 0. */
+typedef struct fcm_scan_desc {
+    fcm_seqs seqs;
+    int c, n_state, groups, dtype, softplus;
+    long long ld_x, ld_dt, ld_b, ld_c, ld_z, ld_y;
+} fcm_scan_desc;
+FCM_API fcm_status fcm_selective_scan(const fcm_scan_desc *desc, const void *x, const void *dt,
+                                      const float *a, const void *bm, const void *cm,
+                                      const float *skip, const void *z, const float *dt_bias,
+                                      const float *state_in, void *y, float *state_out,
+                                      void *stream);
+
+/* Pointwise layer for a few tokens with 4-bit weights and group scales:
+ *     y[t,o] = act(s[o] * sum_k x[t,k] * qs[o,k/group] * (q[o,k] - 8) + b[o])
+ * x [m][in], y [m][out]; qw [out][in/2] bytes, q of an even k in the low four bits of byte k/2 and
+ * the next k's in the high four; qs [out][ceil(in/group)] in the storage dtype; s and b [out]
+ * float32 (NULL: 1, 0).  in is a multiple of 32, group 32, 64 or 128 (the last group may be
+ * short).  The weights are read once for every 16 rows of x. */
+typedef struct fcm_w4_desc {
+    int m, out, in, group, dtype, act;
+    long long ld_x, ld_y;
+} fcm_w4_desc;
+FCM_API fcm_status fcm_w4_matvec(const fcm_w4_desc *desc, const void *x, const void *qw,
+                                 const void *qs, const float *s, const float *b, void *y,
+                                 void *stream);
 
 #ifdef __cplusplus
 }
