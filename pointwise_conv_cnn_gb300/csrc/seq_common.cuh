@@ -39,14 +39,40 @@ __device__ __forceinline__ int state_row(const Seqs &s, int q) {
     return r >= 0 && r < s.slots ? r : -1;
 }
 
-// v / (1 + e^-v).  e^-v overflows to infinity for v < -88 and the quotient is then -0, the limit.
-// The quotient is __fdividef's (2 ulp); its zero for a denominator above 2^126 is that limit too.
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// v / (1 + e^-v).  Where e^-v is infinite, or its reciprocal below the least normal number, the
+// result is -0, the limit.
+__device__ __forceinline__ float silu(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(-kLog2e * v)));
+    return v * r;
+}
 
 // The activations of fcm_act.
 __device__ __forceinline__ float act_seq(float v, int act) {
     return act == FCM_ACT_SILU ? silu(v) : act_apply(v, act);
 }
+
+// VEC consecutive elements, naturally aligned, as stored.  Plain loads: states are read and
+// written by one kernel, and activations may just have been written by the kernel before.
+template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Vec {
+    T e[VEC];
+    __device__ __forceinline__ void get(float (&out)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < VEC; i++) out[i] = Storage<T>::to_f(e[i]);
+    }
+    __device__ __forceinline__ void put(const float (&in)[VEC]) {
+#pragma unroll
+        for (int i = 0; i < VEC; i++) e[i] = Storage<T>::from_f(in[i]);
+    }
+};
 
 // ------------------------------------------------------------------------------------- host
 // Checks fcm_seqs; `state` says whether any state tensor was given.

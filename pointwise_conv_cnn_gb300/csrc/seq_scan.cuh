@@ -1,0 +1,597 @@
+// seq_scan.cuh -- the selective scan's prompt kernel.
+//
+//     h[d,n] = exp(D * a[d,n]) * h[d,n] + D * x[t,d] * bm[t,g,n],   D = softplus(dt[t,d] + dt_bias[d])
+//     y[t,d] = (sum_n cm[t,g,n] * h[d,n] + skip[d] * x[t,d]) * silu(z[t,d])
+#pragma once
+
+
+#include "seq_common.cuh"
+#include "tc_common.cuh"
+
+namespace fcm {
+namespace seq {
+
+struct ScanArgs {
+    Seqs q;
+    const void *x, *dt, *bm, *cm, *z;
+    const float *a, *skip, *dt_bias, *state_in;
+    void *y;
+    float *state_out;
+    long long ld_x, ld_dt, ld_b, ld_c, ld_z, ld_y;
+    int c, n, groups, softplus;
+    int cpg;        // channels per group
+    int blocks;     // channel blocks per group
+    int vec16;      // every block's row of x, dt, z, bm, cm starts on 16 bytes
+    int vec2;       // every block's row of y starts on two elements
+};
+
+constexpr int kUnr = 8;   // steps whose sums are stored together
+constexpr int kMaxState = 128;
+
+// ------------------------------------------------------------------ arithmetic
+// Two 32-bit floats in one register pair: the packed forms halve the instructions issued (the
+// multiply-add pipe's rate is the same).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// max(v, 0) + log(1 + e^-|v|) of two values.  log(1 + t) / t on [0, 1] is the polynomial of degree
+// 9 whose largest relative error is least (Remez exchange in 64 bits): 5e-9, with 32-bit
+// arithmetic 2.5 * 2^-24.  So the relative precision stays where v is far below 0.
+__device__ __forceinline__ void softplus2(float &a, float &b) {
+    constexpr float c[10] = {-0.0032440251670777798f, 0.01985146291553974f, -0.05695953592658043f,
+                             0.10603655129671097f, -0.15305592119693756f, 0.1967593878507614f,
+                             -0.24954134225845337f, 0.3332996368408203f, -0.4999990165233612f, 1.0f};
+    const f32x2 t = pack2(ex2(-kLog2e * fabsf(a)), ex2(-kLog2e * fabsf(b)));
+    f32x2 p = pack2(c[0], c[0]);
+#pragma unroll
+    for (int i = 1; i < 10; i++) p = fma2(p, t, pack2(c[i], c[i]));
+    unpack2(fma2(p, t, pack2(fmaxf(a, 0.0f), fmaxf(b, 0.0f))), a, b);
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t local, int rank) {
+    uint32_t addr;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(local), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// ------------------------------------------------------------------ copies to shared memory
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A tile's rows lie 16 bytes further apart than their length, which keeps lanes that read different
+// rows on different banks.  16-byte aligned rows are copied in 16-byte pieces; others in the
+// aligned 4-byte words that hold their bytes, each row at the offset that its address has within
+// a word.  What lies past a tile's rows or a row's elements is left as it was and not used.
+constexpr int row_pitch(int rb) { return (rb < 16 ? 16 : rb) + 16; }
+
+template <int ROWS, int RB>
+__device__ __forceinline__ void copy_words(uint32_t dst, const char *src, long long stride, int rows, int valid, int tid) {
+    constexpr int NP = RB / 4 + 1;
+    for (int i = tid; i < ROWS * NP; i += 128) {
+        const int r = i / NP, p = i % NP;
+        const char *row = src + r * stride;
+        const int rest = (int)(reinterpret_cast<uintptr_t>(row) & 3);
+        if (r < rows && p * 4 < valid + rest) cp_async4(dst + r * row_pitch(RB) + p * 4, row - rest + p * 4);
+    }
+}
+// A barrier of the four warps that do not scan.
+__device__ __forceinline__ void helpers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Two neighbouring elements in shared memory, widened; whole: their address is a multiple of both.
+template <typename T> __device__ __forceinline__ void get_pair(const unsigned char *p, bool whole, float &a, float &b) {
+    if (whole) {
+        if constexpr (sizeof(T) == 4) {
+            const float2 v = *reinterpret_cast<const float2 *>(p);
+            a = v.x, b = v.y;
+        } else {
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
+            if constexpr (std::is_same<T, __half>::value) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+                a = f.x, b = f.y;
+            } else {
+                a = __uint_as_float(v << 16), b = __uint_as_float(v & 0xFFFF0000u);
+            }
+        }
+    } else {
+        a = Storage<T>::to_f(*reinterpret_cast<const T *>(p));
+        b = Storage<T>::to_f(*reinterpret_cast<const T *>(p + sizeof(T)));
+    }
+}
+template <typename T> __device__ __forceinline__ void store_pair(T *p, float a, float b, int have, bool vec2) {
+    if (vec2 && have >= 2) {
+        const float v[2] = {a, b};
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float2 *>(p) = make_float2(a, b);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(v[0], v[1]);
+        } else {
+            *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
+        }
+    } else {
+        if (have >= 1) p[0] = Storage<T>::from_f(a);
+        if (have >= 2) p[1] = Storage<T>::from_f(b);
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+// SPT states per thread, LPC lanes per channel (SPT * LPC >= n; FULL: equal).  Four warps scan:
+// a warp holds 32 / LPC channels, lane = part * channels + channel, so that the lanes that read
+// one part of B and C are neighbours and the read is a broadcast.  Four more warps do what is
+// per channel and token: they load, make the steps D and D * x and widen B and C for the tile
+// behind, and sum the parts' products, gate and store the tile before.
+constexpr int scan_rows(int ch, int np) { return 1024 / ch < 32 ? 1024 / ch : np >= 64 ? 16 : 32; }
+template <typename T, int SPT, int LPC> struct ScanShape {
+    static constexpr int NS = 128, NT = 256;     // scanning threads, threads
+    static constexpr int CHW = 32 / LPC;         // channels per warp
+    static constexpr int CH = 4 * CHW;           // channels per block
+    static constexpr int NP = SPT * LPC;         // states, padded
+    static constexpr int TT = scan_rows(CH, NP);   // rows per tile
+    static constexpr int NST = 5;                // tiles on chip: one of them finished, one scanned,
+                                                 // one prepared, two on their way
+    static constexpr int RBX = CH * (int)sizeof(T), RBN = NP * (int)sizeof(T);
+    static constexpr int X_BYTES = TT * row_pitch(RBX), N_BYTES = TT * row_pitch(RBN);
+    static constexpr int STAGE = 3 * X_BYTES + 2 * N_BYTES;   // x, dt, z, B, C as stored
+    static constexpr int DU = TT * CH * 8;       // D and D * x of a tile
+    static constexpr int BC = TT * 2 * NP * 4;   // B and C of a tile, widened
+    static constexpr int OUT = TT * CH * LPC * 4;
+    static constexpr int JOIN = NS * (SPT + 1) * 4;   // what the parts of a sequence hand on
+    static constexpr int SMEM = NST * STAGE + 2 * (DU + BC + OUT);   // and JOIN where sequences are split
+};
+
+template <typename T, int SPT, int LPC, bool FULL, bool SPLIT>
+__global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
+    typedef ScanShape<T, SPT, LPC> S;
+    constexpr int TT = S::TT, CH = S::CH, CHW = S::CHW, NP = S::NP;
+    static_assert(TT % kUnr == 0, "a batch of steps stays in its tile");
+    extern __shared__ __align__(16) unsigned char smem[];
+
+    tc::pdl_wait();
+    tc::pdl_launch_dependents();
+
+    const int parts = SPLIT ? (int)cluster_size() : 1;
+    const int rank = SPLIT ? (int)(blockIdx.x % parts) : 0;
+    int id = SPLIT ? (int)(blockIdx.x / parts) : (int)blockIdx.x;
+    const int block = id % a.blocks;
+    id /= a.blocks;
+    const int g = id % a.groups, q = id / a.groups;
+    long long start;
+    int len;
+    seq_rows(a.q, q, start, len);
+    const int row = a.state_in || a.state_out ? state_row(a.q, q) : -1;
+    const int valid = min(CH, a.cpg - block * CH);              // the block's channels
+    const long long c0 = (long long)g * a.cpg + block * CH;     // the first one
+    // this part's rows
+    const int per = SPLIT ? ((len + parts - 1) / parts + TT - 1) / TT * TT : len;
+    const int t0 = SPLIT ? min(len, rank * per) : 0, t1 = SPLIT ? min(len, t0 + per) : len;
+    const int tiles = (t1 - t0 + TT - 1) / TT;
+    auto at_du = [&](int k) { return reinterpret_cast<float2 *>(smem + S::NST * S::STAGE + (k & 1) * S::DU); };
+    auto at_bc = [&](int k) { return reinterpret_cast<float *>(smem + S::NST * S::STAGE + 2 * S::DU + (k & 1) * S::BC); };
+    auto at_out = [&](int k) { return reinterpret_cast<float *>(smem + S::NST * S::STAGE + 2 * (S::DU + S::BC) + (k & 1) * S::OUT); };
+
+    if (threadIdx.x < S::NS) {
+        // ---------------------------------------------------------------- scanning warps
+        const int tid = threadIdx.x, lane = tid & 31, part = lane / CHW, n0 = part * SPT;
+        const int cb = (tid >> 5) * CHW + lane % CHW;           // channel in the block
+        const bool live = cb < valid;
+        const size_t at = (size_t)(c0 + (live ? cb : 0)) * a.n + n0;
+        f32x2 av[SPT / 2], h[SPT / 2];   // decays (base 2), states
+        float h0[SPT];
+        {
+            float v[SPT];
+#pragma unroll
+            for (int i = 0; i < SPT; i++) {
+                const bool in = live && (FULL || n0 + i < a.n);
+                v[i] = in ? a.a[at + i] * kLog2e : 0.0f;
+                h0[i] = in && row >= 0 && a.state_in ? a.state_in[(size_t)row * a.c * a.n + at + i] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < SPT / 2; i++) av[i] = pack2(v[2 * i], v[2 * i + 1]);
+        }
+        float sum_d = 0.0f;
+        // the tiles, with or without the products with C
+        auto scan = [&](auto out_tag) {
+            constexpr bool OUT = decltype(out_tag)::value;
+            __syncthreads();
+            for (int k = 0; k < tiles; k++) {
+                const float2 *du = at_du(k) + cb;
+                const float *bc = at_bc(k) + n0;
+                float *out = at_out(k) + cb * LPC + part;
+                auto step = [&](int r) {
+                    const float2 s = du[r * CH];
+                    const f32x2 u2 = pack2(s.y, s.y), d2 = pack2(s.x, s.x);
+                    if (SPLIT && !OUT) sum_d += s.x;
+                    f32x2 acc0 = 0, acc1 = 0;
+#pragma unroll
+                    for (int j = 0; j < SPT / 2; j += 2) {
+                        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(bc + r * 2 * NP + 2 * j);
+                        float e0, e1, e2, e3;
+                        unpack2(mul2(d2, av[j]), e0, e1);
+                        unpack2(mul2(d2, av[j + 1]), e2, e3);
+                        h[j] = fma2(pack2(ex2(e0), ex2(e1)), h[j], mul2(u2, b2.x));
+                        h[j + 1] = fma2(pack2(ex2(e2), ex2(e3)), h[j + 1], mul2(u2, b2.y));
+                        if (OUT) {
+                            const ulonglong2 c2 = *reinterpret_cast<const ulonglong2 *>(bc + r * 2 * NP + NP + 2 * j);
+                            f32x2 s0 = h[j], s1 = h[j + 1];
+                            if (!FULL) {   // a padding state's 0 * infinity stays out of the sum
+                                float p0, p1, p2, p3;
+                                unpack2(s0, p0, p1);
+                                unpack2(s1, p2, p3);
+                                const int n = n0 + 2 * j;
+                                s0 = pack2(n < a.n ? p0 : 0.0f, n + 1 < a.n ? p1 : 0.0f);
+                                s1 = pack2(n + 2 < a.n ? p2 : 0.0f, n + 3 < a.n ? p3 : 0.0f);
+                            }
+                            acc0 = j == 0 ? mul2(s0, c2.x) : fma2(s0, c2.x, acc0);
+                            acc1 = j == 0 ? mul2(s1, c2.y) : fma2(s1, c2.y, acc1);
+                        }
+                    }
+                    float lo, hi;
+                    unpack2(add2(acc0, acc1), lo, hi);
+                    return lo + hi;
+                };
+                const int rows = min(TT, t1 - t0 - k * TT);
+                if (rows == TT) {
+#pragma unroll 1
+                    for (int r = 0; r < TT; r += kUnr) {
+                        float sums[kUnr];   // stored together: a store holds up the loads behind it
+#pragma unroll
+                        for (int i = 0; i < kUnr; i++) sums[i] = step(r + i);
+                        if (OUT)
+#pragma unroll
+                            for (int i = 0; i < kUnr; i++) out[(r + i) * CH * LPC] = sums[i];
+                    }
+                } else {
+#pragma unroll 1
+                    for (int r = 0; r < rows; r++) {
+                        const float sum = step(r);
+                        if (OUT) out[r * CH * LPC] = sum;
+                    }
+                }
+                __syncthreads();
+            }
+        };
+        if constexpr (SPLIT) {
+            // Each part but the last runs from zero; a part's start is the state before the first
+            // one, carried through the parts between: h = exp(a * sum of their steps) * h + theirs.
+            float *join = reinterpret_cast<float *>(smem + S::SMEM);
+#pragma unroll
+            for (int i = 0; i < SPT / 2; i++) h[i] = 0;
+            if (rank + 1 < parts) scan(std::false_type{});
+#pragma unroll
+            for (int i = 0; i < SPT / 2; i++) {
+                float lo, hi;
+                unpack2(h[i], lo, hi);
+                join[2 * i * S::NS + tid] = lo;
+                join[(2 * i + 1) * S::NS + tid] = hi;
+            }
+            join[SPT * S::NS + tid] = sum_d;
+            cluster_sync();
+            const uint32_t join_at = tc::smem_u32(join);
+            for (int p = 0; p < rank; p++) {
+                const float s = ld_cluster(join_at + (SPT * S::NS + tid) * 4, p);
+#pragma unroll
+                for (int i = 0; i < SPT; i++) {
+                    float lo, hi;
+                    unpack2(av[i / 2], lo, hi);
+                    h0[i] = fmaf(ex2(s * (i & 1 ? hi : lo)), h0[i], ld_cluster(join_at + (i * S::NS + tid) * 4, p));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SPT / 2; i++) h[i] = pack2(h0[2 * i], h0[2 * i + 1]);
+        scan(std::true_type{});
+        if (rank == parts - 1 && row >= 0 && a.state_out && live) {
+            float *to = a.state_out + (size_t)row * a.c * a.n + at;
+#pragma unroll
+            for (int i = 0; i < SPT; i++) {
+                float lo, hi;
+                unpack2(h[i / 2], lo, hi);
+                if (FULL || n0 + i < a.n) to[i] = i & 1 ? hi : lo;
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- the others
+        const int tid = threadIdx.x - S::NS;
+        auto help = [&](auto vec_tag) {
+            constexpr bool vec16 = decltype(vec_tag)::value;
+            constexpr int E = (int)sizeof(T), NST = S::NST, PITCHX = row_pitch(S::RBX), PITCHN = row_pitch(S::RBN);
+            const uint32_t sm = tc::smem_u32(smem);
+            const long long bx = a.ld_x * E, bdt = a.ld_dt * E, bz = a.ld_z * E, bb = a.ld_b * E, bc = a.ld_c * E;
+            const long long first = start + t0;
+            const char *px = static_cast<const char *>(a.x) + first * bx + c0 * E;
+            const char *pdt = static_cast<const char *>(a.dt) + first * bdt + c0 * E;
+            const char *pz = static_cast<const char *>(a.z) + (a.z ? first * bz + c0 * E : 0);
+            const char *pb = static_cast<const char *>(a.bm) + first * bb + (long long)g * a.n * E;
+            const char *pc = static_cast<const char *>(a.cm) + first * bc + (long long)g * a.n * E;
+
+            // ---- copies: a tile's rows, asynchronously, two tiles ahead of their use
+            constexpr int NPX = S::RBX < 16 ? 1 : S::RBX / 16, NPN = S::RBN < 16 ? 1 : S::RBN / 16;   // pieces of a row
+            constexpr int RX = 128 / NPX < TT ? 128 / NPX : TT, RN = 128 / NPN < TT ? 128 / NPN : TT; // rows at once
+            const int rx = tid / NPX, qx = tid % NPX * 16, rn = tid / NPN, qn = tid % NPN * 16;
+            const int nx = rx < TT ? max(0, min(16, valid * E - qx)) : 0, nn = rn < TT ? max(0, min(16, a.n * E - qn)) : 0;
+            auto copy = [&](auto rows_tag, auto pitch_tag, uint32_t to, const char *from, long long stride, int r, int n, int rows) {
+                constexpr int R = decltype(rows_tag)::value, PITCH = decltype(pitch_tag)::value;
+                if (n > 0) {
+#pragma unroll
+                    for (int i = 0; i < TT; i += R)
+                        if (r + i < rows) cp_async16(to + i * PITCH, from + i * stride, n);
+                }
+            };
+            typedef std::integral_constant<int, RX> RowsX;
+            typedef std::integral_constant<int, RN> RowsN;
+            typedef std::integral_constant<int, PITCHX> PitchX;
+            typedef std::integral_constant<int, PITCHN> PitchN;
+            const char *sx = px + rx * bx + qx, *sdt = pdt + rx * bdt + qx, *sz = pz + rx * bz + qx;
+            const char *sb = pb + rn * bb + qn, *sc = pc + rn * bc + qn;
+            auto stage = [&](int k, bool with_out) {
+                if (k < tiles) {
+                    const uint32_t at = sm + (k % NST) * S::STAGE;
+                    const int rows = t1 - t0 - k * TT;
+                    if constexpr (vec16) {
+                        const uint32_t ax = at + rx * PITCHX + qx, an = at + 3 * S::X_BYTES + rn * PITCHN + qn;
+                        copy(RowsX{}, PitchX{}, ax, sx, bx, rx, nx, rows);
+                        copy(RowsX{}, PitchX{}, ax + S::X_BYTES, sdt, bdt, rx, nx, rows);
+                        copy(RowsN{}, PitchN{}, an, sb, bb, rn, nn, rows);
+                        if (with_out) {
+                            if (a.z) copy(RowsX{}, PitchX{}, ax + 2 * S::X_BYTES, sz, bz, rx, nx, rows);
+                            copy(RowsN{}, PitchN{}, an + S::N_BYTES, sc, bc, rn, nn, rows);
+                        }
+                        sx += TT * bx, sdt += TT * bdt, sz += TT * bz, sb += TT * bb, sc += TT * bc;
+                    } else {
+                        const long long t = (long long)k * TT;
+                        copy_words<TT, S::RBX>(at, px + t * bx, bx, rows, valid * E, tid);
+                        copy_words<TT, S::RBX>(at + S::X_BYTES, pdt + t * bdt, bdt, rows, valid * E, tid);
+                        copy_words<TT, S::RBN>(at + 3 * S::X_BYTES, pb + t * bb, bb, rows, a.n * E, tid);
+                        if (with_out) {
+                            if (a.z) copy_words<TT, S::RBX>(at + 2 * S::X_BYTES, pz + t * bz, bz, rows, valid * E, tid);
+                            copy_words<TT, S::RBN>(at + 3 * S::X_BYTES + S::N_BYTES, pc + t * bc, bc, rows, a.n * E, tid);
+                        }
+                    }
+                }
+                cp_commit();
+            };
+
+            // ---- channel pairs of a tile, and quads of states
+            constexpr int PR = CH / 2, RS = 128 / PR < TT ? 128 / PR : TT, IT = TT / RS;
+            constexpr int QR = NP / 4, QS = 128 / QR < TT ? 128 / QR : TT, QT = TT / QS;
+            const int ch = tid % PR * 2, r0 = tid / PR, have = r0 < RS ? valid - ch : 0;
+            const int n4 = tid % QR * 4, rq = tid / QR;
+            float bias[2] = {0.0f, 0.0f}, skip[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                if (have > i) {
+                    if (a.dt_bias) bias[i] = a.dt_bias[c0 + ch + i];
+                    if (a.skip) skip[i] = a.skip[c0 + ch + i];
+                }
+            T *py = static_cast<T *>(a.y) + (first + r0) * a.ld_y + c0 + ch;
+            // where row r of a tile starts within its place: copies of words keep the address's rest
+            auto rest = [&](const char *p, long long stride, int r) {
+                return vec16 ? 0u : (uint32_t)((reinterpret_cast<uintptr_t>(p) + (uintptr_t)(r * stride)) & 3);
+            };
+            auto prepare = [&](int k, bool with_c) {
+                const unsigned char *raw = smem + (k % NST) * S::STAGE;
+                if (r0 < RS) {
+                    float x[IT][2], d[IT][2];
+                    if constexpr (vec16) {
+#pragma unroll
+                        for (int i = 0; i < IT; i++) {
+                            const unsigned char *p = raw + (r0 + i * RS) * PITCHX + ch * E;
+                            get_pair<T>(p, true, x[i][0], x[i][1]);
+                            get_pair<T>(p + S::X_BYTES, true, d[i][0], d[i][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < IT; i++) {
+                            const int r = r0 + i * RS;
+                            const unsigned char *p = raw + r * PITCHX + ch * E;
+                            get_pair<T>(p + rest(px, bx, k * TT + r), false, x[i][0], x[i][1]);
+                            get_pair<T>(p + S::X_BYTES + rest(pdt, bdt, k * TT + r), false, d[i][0], d[i][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < IT; i++) d[i][0] += bias[0], d[i][1] += bias[1];
+                    if (a.softplus)
+#pragma unroll
+                        for (int i = 0; i < IT; i++) softplus2(d[i][0], d[i][1]);
+                    float2 *du = at_du(k);
+#pragma unroll
+                    for (int i = 0; i < IT; i++)
+                        *reinterpret_cast<float4 *>(du + (r0 + i * RS) * CH + ch) =
+                            make_float4(d[i][0], d[i][0] * x[i][0], d[i][1], d[i][1] * x[i][1]);
+                }
+                if (rq < QS) {
+                    float *to = at_bc(k);
+#pragma unroll
+                    for (int which = 0; which < 2; which++) {
+                        if (which && !with_c) break;
+                        const unsigned char *from = raw + 3 * S::X_BYTES + which * S::N_BYTES + n4 * E;
+#pragma unroll
+                        for (int i = 0; i < QT; i++) {
+                            const int r = rq + i * QS;
+                            const unsigned char *p = from + r * PITCHN;
+                            if (!vec16) p += which ? rest(pc, bc, k * TT + r) : rest(pb, bb, k * TT + r);
+                            float4 v;
+                            get_pair<T>(p, vec16, v.x, v.y);
+                            get_pair<T>(p + 2 * E, vec16, v.z, v.w);
+                            if (!FULL) {   // padding states: nothing in, nothing out
+                                v.x = n4 < a.n ? v.x : 0.0f, v.y = n4 + 1 < a.n ? v.y : 0.0f;
+                                v.z = n4 + 2 < a.n ? v.z : 0.0f, v.w = n4 + 3 < a.n ? v.w : 0.0f;
+                            }
+                            *reinterpret_cast<float4 *>(to + r * 2 * NP + which * NP + n4) = v;
+                        }
+                    }
+                }
+            };
+            auto finish = [&](int k) {
+                if (r0 >= RS) return;
+                const unsigned char *raw = smem + (k % NST) * S::STAGE;
+                const float *out = at_out(k) + ch * LPC;
+                float o[IT][2];
+#pragma unroll
+                for (int i = 0; i < IT; i++) {
+                    const float *p = out + (r0 + i * RS) * CH * LPC;
+                    if constexpr (LPC == 1) {
+                        const float2 v = *reinterpret_cast<const float2 *>(p);
+                        o[i][0] = v.x, o[i][1] = v.y;
+                    } else if constexpr (LPC == 2) {
+                        const float4 v = *reinterpret_cast<const float4 *>(p);
+                        o[i][0] = v.x + v.y, o[i][1] = v.z + v.w;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            o[i][c] = 0.0f;
+#pragma unroll
+                            for (int j = 0; j < LPC; j += 4) {
+                                const float4 v = *reinterpret_cast<const float4 *>(p + c * LPC + j);
+                                const float s = (v.x + v.y) + (v.z + v.w);
+                                o[i][c] = j == 0 ? s : o[i][c] + s;
+                            }
+                        }
+                    }
+                }
+                if (a.skip)
+#pragma unroll
+                    for (int i = 0; i < IT; i++) {
+                        const int r = r0 + i * RS;
+                        float x, y;
+                        get_pair<T>(raw + r * PITCHX + ch * E + rest(px, bx, k * TT + r), vec16, x, y);
+                        o[i][0] = fmaf(skip[0], x, o[i][0]);
+                        o[i][1] = fmaf(skip[1], y, o[i][1]);
+                    }
+                if (a.z)
+#pragma unroll
+                    for (int i = 0; i < IT; i++) {
+                        const int r = r0 + i * RS;
+                        float x, y;
+                        get_pair<T>(raw + 2 * S::X_BYTES + r * PITCHX + ch * E + rest(pz, bz, k * TT + r), vec16, x, y);
+                        o[i][0] *= silu(x);
+                        o[i][1] *= silu(y);
+                    }
+                const int left = t1 - t0 - k * TT;
+#pragma unroll
+                for (int i = 0; i < IT; i++)
+                    if (r0 + i * RS < left)
+                        store_pair<T>(py + ((long long)k * TT + i * RS) * a.ld_y, o[i][0], o[i][1], have, a.vec2);
+            };
+            // Tile k is scanned while tile k + 1 is prepared and tile k - 1 finished; tile k + 2 has
+            // arrived at the end of that, tile k + 3 is on its way into the place of tile k - 2.
+            auto serve = [&](bool with_out) {
+                sx = px + rx * bx + qx, sdt = pdt + rx * bdt + qx, sz = pz + rx * bz + qx;
+                sb = pb + rn * bb + qn, sc = pc + rn * bc + qn;
+                for (int k = 0; k < 3; k++) stage(k, with_out);
+                cp_wait<1>();                       // tiles 0 and 1
+                helpers_sync();
+                if (tiles > 0) prepare(0, with_out);
+                __syncthreads();
+                for (int k = 0; k < tiles; k++) {
+                    stage(k + 3, with_out);
+                    if (k + 1 < tiles) prepare(k + 1, with_out);
+                    if (with_out && k > 0) finish(k - 1);
+                    cp_wait<1>();                   // tile k + 2
+                    __syncthreads();
+                }
+                if (with_out && tiles > 0) finish(tiles - 1);
+            };
+            if constexpr (SPLIT) {
+                if (rank + 1 < parts) serve(false);
+                cluster_sync();
+            }
+            serve(true);
+        };
+        if (a.vec16) help(std::true_type{});
+        else help(std::false_type{});
+    }
+    if constexpr (SPLIT) cluster_sync();   // the others may still be reading this block's part
+}
+
+// Shared memory of a block of one shape.
+template <typename T> constexpr int scan_smem(int spt, int lpc) {
+    const int ch = 128 / lpc, np = spt * lpc, tt = scan_rows(ch, np), e = (int)sizeof(T);
+    return 5 * tt * (3 * row_pitch(ch * e) + 2 * row_pitch(np * e)) + 2 * tt * (ch * 8 + np * 8 + 128 * 4);
+}
+
+// Launches the kernel of one shape; `parts` blocks of a cluster share a sequence.
+template <typename T, int SPT, int LPC, bool FULL>
+cudaError_t launch_scan_shape(ScanArgs a, int parts, cudaStream_t st) {
+    typedef ScanShape<T, SPT, LPC> S;
+    static_assert(S::SMEM == scan_smem<T>(SPT, LPC), "");
+    static std::atomic<unsigned long long> attr_ctx[2];
+    a.blocks = (a.cpg + S::CH - 1) / S::CH;
+    const long long grid = (long long)a.q.n_seq * a.groups * a.blocks * parts;
+    if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+    const int smem = S::SMEM + (parts > 1 ? S::JOIN : 0);
+    void (*kernel)(ScanArgs) = parts > 1 ? scan_kernel<T, SPT, LPC, FULL, true>
+                                         : scan_kernel<T, SPT, LPC, FULL, false>;
+    if (smem > 48 * 1024) {   // raised once per context, as for the tensor-core kernels
+        std::atomic<unsigned long long> &known = attr_ctx[parts > 1];
+        const unsigned long long ctx = fcm_current_ctx_id();
+        if (ctx == 0 || known.load(std::memory_order_relaxed) != ctx) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            known.store(ctx, std::memory_order_relaxed);
+        }
+    }
+    return launch(kernel, dim3((unsigned)grid), S::NT, (size_t)smem, st, a, parts);
+}
+
+// Shapes by states per thread and lanes per channel (seq_scan_inst_*.cu).
+template <typename T> cudaError_t launch_scan(const ScanArgs &a, int spt, int lpc, int parts, cudaStream_t st);
+
+#define FCM_SCAN_INSTANTIATE(T)                                                                      \
+    template <>                                                                                      \
+    cudaError_t launch_scan<T>(const ScanArgs &a, int spt, int lpc, int parts, cudaStream_t st) {    \
+        const bool full = a.n == spt * lpc;                                                          \
+        switch (spt * 256 + lpc * 2 + full) {                                                        \
+            FCM_SCAN_CASE(T, 4, 1, 0) FCM_SCAN_CASE(T, 4, 2, 0) FCM_SCAN_CASE(T, 4, 4, 0)            \
+            FCM_SCAN_CASE(T, 4, 8, 0) FCM_SCAN_CASE(T, 8, 8, 0) FCM_SCAN_CASE(T, 8, 16, 0)           \
+            FCM_SCAN_CASE(T, 4, 1, 1) FCM_SCAN_CASE(T, 4, 2, 1) FCM_SCAN_CASE(T, 4, 4, 1)            \
+            FCM_SCAN_CASE(T, 4, 8, 1) FCM_SCAN_CASE(T, 8, 8, 1) FCM_SCAN_CASE(T, 8, 16, 1)           \
+            FCM_SCAN_CASE(T, 8, 2, 1) FCM_SCAN_CASE(T, 8, 4, 1) FCM_SCAN_CASE(T, 16, 1, 1)           \
+        }                                                                                            \
+        return cudaErrorInvalidValue;                                                                \
+    }
+#define FCM_SCAN_CASE(T, SPT, LPC, FULL) \
+    case SPT * 256 + LPC * 2 + FULL: return launch_scan_shape<T, SPT, LPC, FULL>(a, parts, st);
+
+}  // namespace seq
+}  // namespace fcm
