@@ -22,50 +22,164 @@ struct ConvArgs {
 
 constexpr int kMaxTaps = 8;
 
-// One thread: one channel, a.rows consecutive rows of one sequence.
-template <typename T>
+// One thread: VEC neighbouring channels (16 bytes, or one), a.rows consecutive rows of one
+// sequence.  The K - 1 rows before them are read again from the neighbour's tile or are the cached
+// ones; from there each row is read once and kept in registers for its K uses.  The thread of a
+// sequence's first rows also replaces the cached rows, which it has read by then, so that
+// state_out may be state_in.
+template <typename T, int VEC, int K>
 __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
+    typedef Vec<T, VEC> V;
+    constexpr int H = K - 1, U = 4;   // rows before, rows loaded at once
     tc::pdl_wait();
     tc::pdl_launch_dependents();
     const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (id >= a.threads) return;
-    const int d = (int)(id % a.c);
-    const long long rest = id / a.c;
+    const int cg = a.c / VEC, d = (int)(id % cg) * VEC;
+    const long long rest = id / cg;
     const int tile = (int)(rest % a.tiles), q = (int)(rest / a.tiles);
     long long start;
     int len;
     seq_rows(a.q, q, start, len);
-    const int i0 = tile * a.rows, h = a.k - 1;
+    const int i0 = tile * a.rows, i1 = min(len, i0 + a.rows);
+    if (tile > 0 && i0 >= i1) return;
     const T *x = static_cast<const T *>(a.x) + d + start * a.ld_x;
     T *y = static_cast<T *>(a.y) + d + start * a.ld_y;
-    const int row = h > 0 && (a.state_in || a.state_out) ? state_row(a.q, q) : -1;
-    const size_t at = row < 0 ? 0 : (size_t)row * h * a.c + d;
-    T old[kMaxTaps - 1];   // the cached rows, read before any of them is replaced
-    for (int j = 0; j < kMaxTaps - 1; j++) {
-        old[j] = Storage<T>::from_f(0.0f);
-        if (j < h && row >= 0 && a.state_in && tile == 0)
-            old[j] = static_cast<const T *>(a.state_in)[at + (size_t)j * a.c];
+
+    float win[H + U][VEC];   // rows i - H .. i + U - 1
+    V old[K > 1 ? H : 1];    // the cached rows
+    int row = -1;
+    size_t at = 0;
+    if (K > 1) {
+        if (tile == 0) {
+            if (a.state_in || a.state_out) row = state_row(a.q, q);
+            at = (size_t)(row < 0 ? 0 : row) * H * a.c + d;
+#pragma unroll
+            for (int j = 0; j < H; j++) {
+#pragma unroll
+                for (int v = 0; v < VEC; v++) old[j].e[v] = Storage<T>::from_f(0.0f);
+                if (row >= 0 && a.state_in)
+                    old[j] = *reinterpret_cast<const V *>(static_cast<const T *>(a.state_in) + at + (size_t)j * a.c);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < H; j++) old[j] = *reinterpret_cast<const V *>(x + (long long)(i0 - H + j) * a.ld_x);
+        }
+#pragma unroll
+        for (int j = 0; j < H; j++) old[j].get(win[j]);
     }
-    auto in = [&](int i) -> T {   // place i of the sequence; places before 0 are the cached rows
-        if (i >= 0) return x[(long long)i * a.ld_x];
-        T v = old[0];
-        for (int j = 1; j < kMaxTaps - 1; j++)
-            if (j == i + h) v = old[j];
-        return v;
+    float w[VEC * K], s[VEC], b[VEC];
+    {
+        constexpr int PIECE = VEC * K * sizeof(T) % 16 == 0 ? 16 / (int)sizeof(T) : 1;   // w's own order
+#pragma unroll
+        for (int j = 0; j < VEC * K; j += PIECE) {
+            const Vec<T, PIECE> p = *reinterpret_cast<const Vec<T, PIECE> *>(static_cast<const T *>(a.w) + (size_t)d * K + j);
+#pragma unroll
+            for (int v = 0; v < PIECE; v++) w[j + v] = Storage<T>::to_f(p.e[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; v++) s[v] = 1.0f, b[v] = 0.0f;
+        constexpr int F = VEC % 4 == 0 ? 4 : 1;
+#pragma unroll
+        for (int v = 0; v < VEC; v += F) {
+            if (a.s) {
+                const Vec<float, F> p = *reinterpret_cast<const Vec<float, F> *>(a.s + d + v);
+#pragma unroll
+                for (int e = 0; e < F; e++) s[v + e] = p.e[e];
+            }
+            if (a.b) {
+                const Vec<float, F> p = *reinterpret_cast<const Vec<float, F> *>(a.b + d + v);
+#pragma unroll
+                for (int e = 0; e < F; e++) b[v + e] = p.e[e];
+            }
+        }
+    }
+    // The state after: the last H places, of which those before 0 are cached rows.  All are read
+    // before any is written.
+    if (K > 1 && row >= 0 && a.state_out) {
+        V last[K > 1 ? H : 1];
+#pragma unroll
+        for (int j = 0; j < H; j++) {
+            const int i = len - H + j;
+            V none;
+#pragma unroll
+            for (int v = 0; v < VEC; v++) none.e[v] = Storage<T>::from_f(0.0f);
+            last[j] = none;
+            const T *from = i >= 0 ? x + (long long)i * a.ld_x
+                                   : static_cast<const T *>(a.state_in) + at + (size_t)(i + H) * a.c;
+            if (i >= 0 || a.state_in) last[j] = *reinterpret_cast<const V *>(from);
+        }
+#pragma unroll
+        for (int j = 0; j < H; j++)
+            *reinterpret_cast<V *>(static_cast<T *>(a.state_out) + at + (size_t)j * a.c) = last[j];
+    }
+    auto rows = [&](int i, int n) {   // rows i .. i + n - 1, n <= U
+        V in[U];
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (u < n) in[u] = *reinterpret_cast<const V *>(x + (long long)(i + u) * a.ld_x);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (u >= n) break;
+            in[u].get(win[H + u]);
+            float o[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                float acc = 0.0f;
+#pragma unroll
+                for (int j = 0; j < K; j++) acc = fmaf(w[v * K + j], win[u + j][v], acc);
+                o[v] = fmaf(s[v], acc, b[v]);
+            }
+            if (a.act == FCM_ACT_SILU) {
+#pragma unroll
+                for (int v = 0; v < VEC; v++) o[v] = silu(o[v]);
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; v++) o[v] = act_apply(o[v], a.act);
+            }
+            V out;
+            out.put(o);
+            *reinterpret_cast<V *>(y + (long long)(i + u) * a.ld_y) = out;
+        }
+#pragma unroll
+        for (int j = 0; j < H; j++)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) win[j][v] = win[U + j][v];
     };
-    float w[kMaxTaps];
-    for (int j = 0; j < kMaxTaps; j++)
-        w[j] = j < a.k ? Storage<T>::to_f(static_cast<const T *>(a.w)[(size_t)d * a.k + j]) : 0.0f;
-    const float s = a.s ? a.s[d] : 1.0f, b = a.b ? a.b[d] : 0.0f;
-    for (int i = i0; i < min(len, i0 + a.rows); i++) {
-        float acc = 0.0f;
-        for (int j = 0; j < kMaxTaps; j++)
-            if (j < a.k) acc = fmaf(w[j], Storage<T>::to_f(in(i + j - h)), acc);
-        y[(long long)i * a.ld_y] = Storage<T>::from_f(act_seq(fmaf(s, acc, b), a.act));
+    int i = i0;
+    for (; i + U <= i1; i += U) rows(i, U);
+    if (i < i1) rows(i, i1 - i);
+}
+
+template <typename T, int VEC>
+static void (*pick_conv(int k))(ConvArgs) {
+    switch (k) {
+    case 1: return causal_conv_kernel<T, VEC, 1>;
+    case 2: return causal_conv_kernel<T, VEC, 2>;
+    case 3: return causal_conv_kernel<T, VEC, 3>;
+    case 4: return causal_conv_kernel<T, VEC, 4>;
+    case 5: return causal_conv_kernel<T, VEC, 5>;
+    case 6: return causal_conv_kernel<T, VEC, 6>;
+    case 7: return causal_conv_kernel<T, VEC, 7>;
+    default: return causal_conv_kernel<T, VEC, 8>;
     }
-    if (tile == 0 && row >= 0 && a.state_out)
-        for (int j = 0; j < h; j++)
-            static_cast<T *>(a.state_out)[at + (size_t)j * a.c] = in(len - h + j);
+}
+
+template <typename T>
+static cudaError_t run_conv(ConvArgs a, int sms, cudaStream_t st) {
+    constexpr int VEC = 16 / (int)sizeof(T);
+    const bool vec = ((a.c | a.ld_x | a.ld_y) % VEC) == 0 && aligned16(a.x) && aligned16(a.w) && aligned16(a.s) &&
+                     aligned16(a.b) && aligned16(a.state_in) && aligned16(a.y) && aligned16(a.state_out);
+    const long long cg = vec ? a.c / VEC : a.c, all = (long long)a.q.n_seq * cg;
+    // no fewer rows than cached ones: only the first tile's window reaches those
+    const int least = a.k > 5 ? 8 : 4;
+    a.rows = 32;
+    while (a.rows > least && all * ((a.q.max_len + a.rows - 1) / a.rows) < (long long)sms * 1024) a.rows /= 2;
+    a.tiles = a.q.max_len ? (a.q.max_len + a.rows - 1) / a.rows : 1;
+    a.threads = all * a.tiles;
+    const long long blocks = (a.threads + 127) / 128;
+    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+    return launch(vec ? pick_conv<T, VEC>(a.k) : pick_conv<T, 1>(a.k), dim3((unsigned)blocks), 128, 0, st, a);
 }
 
 }  // namespace seq
@@ -116,16 +230,10 @@ extern "C" fcm_status fcm_causal_conv(const fcm_causal_conv_desc *desc, const vo
 
     a.x = x, a.w = w, a.s = s, a.b = b, a.state_in = state_in, a.y = y, a.state_out = state_out;
     a.ld_x = d.ld_x, a.ld_y = d.ld_y, a.c = d.c, a.k = d.ksize, a.act = d.act;
-    a.rows = 16;
-    a.tiles = a.q.max_len ? (a.q.max_len + a.rows - 1) / a.rows : 1;
-    a.threads = (long long)a.q.n_seq * a.tiles * a.c;
-    const long long blocks = (a.threads + 127) / 128;
-    if (blocks > 0x7FFFFFFFLL) return fcm_fail(FCM_ERR_UNSUPPORTED, "more than 2^31 thread blocks");
-    void (*kernel)(seq::ConvArgs) = d.dtype == FCM_F32   ? seq::causal_conv_kernel<float>
-                                    : d.dtype == FCM_F16 ? seq::causal_conv_kernel<__half>
-                                                         : seq::causal_conv_kernel<__nv_bfloat16>;
-    const cudaError_t ce = seq::launch(kernel, dim3((unsigned)blocks), 128, 0,
-                                       static_cast<cudaStream_t>(stream), a);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t ce = d.dtype == FCM_F32   ? seq::run_conv<float>(a, sms, cs)
+                           : d.dtype == FCM_F16 ? seq::run_conv<__half>(a, sms, cs)
+                                                : seq::run_conv<__nv_bfloat16>(a, sms, cs);
     if (ce != cudaSuccess) return fcm_fail(FCM_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(ce));
     return FCM_OK;
 }
