@@ -12,33 +12,159 @@ struct W4Args {
     const float *s, *b;
     void *y;
     long long ld_x, ld_y;
-    int m, out, in, group, act;
+    int m, out, in, act;
+    int units;   // groups of inputs
 };
 
-// One warp: one output of up to 16 tokens; a lane takes 8 weights of every 256.
+// A 16 x 8 x 16 product on the tensor cores: rows are outputs, columns tokens.
 template <typename T>
-__global__ void __launch_bounds__(128) w4_simple_kernel(const W4Args a) {
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The values of bits [4j, 4j + 4) and [4j + 16, 4j + 20) of q, less 8, in two halves: the bits are
+// put into the mantissa of 1024 (f16) or 128 (bf16), whose last place is 1 there, so the
+// difference is exact.
+template <typename T> __device__ __forceinline__ uint32_t two_weights(uint32_t q, int j) {
+    const uint32_t bits = (q >> (4 * j)) & 0x000F000Fu;
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value) {
+        const uint32_t v = bits | 0x64006400u, o = 0x64086408u;   // 1024 + q, 1032
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(o));
+    } else {
+        const uint32_t v = bits | 0x43004300u, o = 0x43084308u;   // 128 + q, 136
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(o));
+    }
+    return r;
+}
+
+// One block: 16 outputs of up to 8 * NT tokens; its warps share the inputs' groups.  A lane of row
+// r = lane / 4 and quarter t = lane % 4 holds the weights of rows r and r + 8 in quarter t of a
+// group, and the inputs of token r there.  The product's inner index may run in any order as
+// long as both sides follow it: a 32-bit word of eight weights gives the pairs (0,4), (1,5),
+// (2,6), (3,7) with a shift and a mask each, and the inputs are paired alike.  So weights go
+// from memory to the tensor cores as whole numbers, without a detour, and a group's sum is
+// scaled in 32 bits.  XV: x's rows are 16-byte aligned.
+template <typename T, int G, int NT, bool XV>
+__global__ void __launch_bounds__(512) w4_kernel(const W4Args a) {
+    constexpr int WORDS = G / 32;   // words per lane and group
+    constexpr int UB = 128 / G * 4; // groups loaded at once: 64 bytes of each row... of each lane
+    extern __shared__ float red[];
     tc::pdl_wait();
     tc::pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, o = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (o >= a.out) return;
-    const int groups = (a.in + a.group - 1) / a.group;
-    for (int t = blockIdx.y * 16; t < min(a.m, (int)blockIdx.y * 16 + 16); t++) {
-        const T *x = static_cast<const T *>(a.x) + (long long)t * a.ld_x;
-        float acc = 0.0f;
-        for (int k = lane * 8; k < a.in; k += 256) {
-            const uint32_t q = *reinterpret_cast<const uint32_t *>(
-                static_cast<const uint8_t *>(a.qw) + ((size_t)o * a.in + k) / 2);
-            float sum = 0.0f;
-            for (int j = 0; j < 8; j++)
-                sum = fmaf(Storage<T>::to_f(x[k + j]), (float)((int)(q >> (4 * j) & 15) - 8), sum);
-            acc = fmaf(sum, Storage<T>::to_f(static_cast<const T *>(a.qs)[(size_t)o * groups + k / a.group]), acc);
-        }
-        for (int i = 16; i; i >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, i);
-        if (lane == 0)
-            static_cast<T *>(a.y)[(long long)t * a.ld_y + o] = Storage<T>::from_f(
-                act_seq(fmaf(a.s ? a.s[o] : 1.0f, acc, a.b ? a.b[o] : 0.0f), a.act));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int r = lane >> 2, t = lane & 3, o0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
+    // rows past the last output repeat it
+    const int oa = min(o0 + r, a.out - 1), ob = min(o0 + r + 8, a.out - 1);
+    const uint8_t *wa = static_cast<const uint8_t *>(a.qw) + (size_t)oa * (a.in / 2) + t * (G / 8);
+    const uint8_t *wb = static_cast<const uint8_t *>(a.qw) + (size_t)ob * (a.in / 2) + t * (G / 8);
+    const T *sa = static_cast<const T *>(a.qs) + (size_t)oa * a.units, *sb = static_cast<const T *>(a.qs) + (size_t)ob * a.units;
+    const T *x[NT];
+    bool token[NT];
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
+        token[i] = m0 + i * 8 + r < a.m;
+        x[i] = static_cast<const T *>(a.x) + (long long)(token[i] ? m0 + i * 8 + r : m0) * a.ld_x + t * (G / 4);
     }
+    float sum[NT][4] = {};
+    struct alignas(4 * WORDS) Words {
+        uint32_t w[WORDS];
+    };
+    auto group = [&](int u, const Words &qa, const Words &qb, float fa, float fb, bool in) {
+        float c[NT][4] = {};
+#pragma unroll
+        for (int w = 0; w < WORDS; w++) {
+            uint32_t b[NT][4];
+#pragma unroll
+            for (int i = 0; i < NT; i++) {
+                const T *p = x[i] + (size_t)u * G + w * 8;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (token[i] && in) {
+                    if (XV) {
+                        v = *reinterpret_cast<const uint4 *>(p);
+                    } else {
+                        const unsigned short *e = reinterpret_cast<const unsigned short *>(p);
+                        v = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                       e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                    }
+                }
+                b[i][0] = __byte_perm(v.x, v.z, 0x5410), b[i][1] = __byte_perm(v.x, v.z, 0x7632);
+                b[i][2] = __byte_perm(v.y, v.w, 0x5410), b[i][3] = __byte_perm(v.y, v.w, 0x7632);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t f[4] = {two_weights<T>(qa.w[w], 2 * h), two_weights<T>(qb.w[w], 2 * h),
+                                       two_weights<T>(qa.w[w], 2 * h + 1), two_weights<T>(qb.w[w], 2 * h + 1)};
+#pragma unroll
+                for (int i = 0; i < NT; i++) mma16816<T>(c[i], f, b[i][2 * h], b[i][2 * h + 1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+            sum[i][0] = fmaf(c[i][0], fa, sum[i][0]);
+            sum[i][1] = fmaf(c[i][1], fa, sum[i][1]);
+            sum[i][2] = fmaf(c[i][2], fb, sum[i][2]);
+            sum[i][3] = fmaf(c[i][3], fb, sum[i][3]);
+        }
+    };
+    const int whole = a.in / G;   // groups that are not short
+    const int per = (a.units + warps - 1) / warps, u0 = warp * per, u1 = min(a.units, u0 + per);
+    int u = u0;
+    for (; u + UB <= min(u1, whole); u += UB) {
+        Words qa[UB], qb[UB];
+        float fa[UB], fb[UB];
+#pragma unroll
+        for (int i = 0; i < UB; i++) {
+            qa[i] = *reinterpret_cast<const Words *>(wa + (size_t)(u + i) * (G / 2));
+            qb[i] = *reinterpret_cast<const Words *>(wb + (size_t)(u + i) * (G / 2));
+            fa[i] = Storage<T>::to_f(sa[u + i]);
+            fb[i] = Storage<T>::to_f(sb[u + i]);
+        }
+#pragma unroll
+        for (int i = 0; i < UB; i++) group(u + i, qa[i], qb[i], fa[i], fb[i], true);
+    }
+    for (; u < u1; u++) {
+        const bool in = u * G + t * (G / 4) < a.in;   // a short group ends with a lane's quarter
+        Words qa = {}, qb = {};
+        if (in) {
+            qa = *reinterpret_cast<const Words *>(wa + (size_t)u * (G / 2));
+            qb = *reinterpret_cast<const Words *>(wb + (size_t)u * (G / 2));
+        }
+        group(u, qa, qb, Storage<T>::to_f(sa[u]), Storage<T>::to_f(sb[u]), in);
+    }
+    // the warps' sums, in their order
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            red[(warp * NT * 8 + i * 8 + 2 * t + (j & 1)) * 16 + r + (j >> 1) * 8] = sum[i][j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < NT * 128; i += blockDim.x) {
+        const int tok = m0 + i / 16, o = o0 + i % 16;
+        if (tok >= a.m || o >= a.out) continue;
+        float v = 0.0f;
+        for (int w = 0; w < warps; w++) v += red[w * NT * 128 + i];
+        static_cast<T *>(a.y)[(long long)tok * a.ld_y + o] = Storage<T>::from_f(
+            act_seq(fmaf(a.s ? a.s[o] : 1.0f, v, a.b ? a.b[o] : 0.0f), a.act));
+    }
+}
+
+template <typename T, int G>
+static cudaError_t run_w4(const W4Args &a, int sms, cudaStream_t st) {
+    const unsigned tiles = (unsigned)((a.out + 15) / 16), gy = (unsigned)((a.m + 15) / 16);
+    int warps = tiles * gy >= 2u * sms ? 8 : 16;
+    while (warps > 4 && warps / 2 >= a.units) warps /= 2;
+    const bool xv = aligned16(a.x) && a.ld_x % 8 == 0, wide = a.m > 8;
+    void (*kernel)(W4Args) = wide ? (xv ? w4_kernel<T, G, 2, true> : w4_kernel<T, G, 2, false>)
+                                  : (xv ? w4_kernel<T, G, 1, true> : w4_kernel<T, G, 1, false>);
+    return launch(kernel, dim3(tiles, gy), warps * 32, (size_t)warps * (wide ? 256 : 128) * 4, st, a);
 }
 
 }  // namespace seq
@@ -77,11 +203,18 @@ extern "C" fcm_status fcm_w4_matvec(const fcm_w4_desc *desc, const void *x, cons
     int sms;
     if ((st = seq::current_device(&sms)) != FCM_OK) return st;
 
-    const seq::W4Args a = {x, qw, qs, s, b, y, d.ld_x, d.ld_y, d.m, d.out, d.in, d.group, d.act};
-    const dim3 grid((unsigned)((d.out + 3) / 4), (unsigned)((d.m + 15) / 16));
-    const cudaError_t ce = seq::launch(d.dtype == FCM_F16 ? seq::w4_simple_kernel<__half>
-                                                          : seq::w4_simple_kernel<__nv_bfloat16>,
-                                       grid, 128, 0, static_cast<cudaStream_t>(stream), a);
+    const seq::W4Args a = {x, qw, qs, s, b, y, d.ld_x, d.ld_y, d.m, d.out, d.in, d.act,
+                           (d.in + d.group - 1) / d.group};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    cudaError_t ce;
+    if (d.dtype == FCM_F16)
+        ce = d.group == 128  ? seq::run_w4<__half, 128>(a, sms, cs)
+             : d.group == 64 ? seq::run_w4<__half, 64>(a, sms, cs)
+                             : seq::run_w4<__half, 32>(a, sms, cs);
+    else
+        ce = d.group == 128  ? seq::run_w4<__nv_bfloat16, 128>(a, sms, cs)
+             : d.group == 64 ? seq::run_w4<__nv_bfloat16, 64>(a, sms, cs)
+                             : seq::run_w4<__nv_bfloat16, 32>(a, sms, cs);
     if (ce != cudaSuccess) return fcm_fail(FCM_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(ce));
     return FCM_OK;
 }
