@@ -11,6 +11,7 @@ fcm_status check_seqs(const fcm_seqs &s, bool state, Seqs *out) {
         return fcm_fail(FCM_ERR_INVALID_ARG, "negative tokens, n_seq or max_len");
     if (s.tokens > (1LL << 31) - 1)
         return fcm_fail(FCM_ERR_UNSUPPORTED, "%lld tokens; at most 2^31 - 1", s.tokens);
+    if (s.n_seq > 1 << 30) return fcm_fail(FCM_ERR_UNSUPPORTED, "%d sequences; at most 2^30", s.n_seq);
     if (!s.seq_start && s.tokens != (long long)s.n_seq * s.max_len)
         return fcm_fail(FCM_ERR_INVALID_ARG,
                         "%lld tokens are not n_seq %d times max_len %d (no seq_start)", s.tokens,
@@ -33,9 +34,9 @@ fcm_status check_seqs(const fcm_seqs &s, bool state, Seqs *out) {
 
 fcm_status check_ld(long long *ld, long long row, const char *name) {
     if (*ld == 0) *ld = row;
-    if (*ld < row || *ld > (1LL << 31))
+    if (*ld < row || *ld > 0x7FFFFFFFLL)
         return fcm_fail(FCM_ERR_INVALID_ARG, "%s %lld: rows of %lld elements need at least that, "
-                        "and at most 2^31", name, *ld, row);
+                        "and at most 2^31 - 1", name, *ld, row);
     return FCM_OK;
 }
 

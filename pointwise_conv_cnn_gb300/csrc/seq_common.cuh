@@ -88,7 +88,7 @@ bool rows_overlap(const void *a, long long lda, long long ca, const void *b, lon
 // The current device's SM count; an error unless it is a compute capability 10.3 device.
 fcm_status current_device(int *num_sms);
 
-inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+__host__ __device__ inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Launch with programmatic stream serialization allowed: the kernels wait for the previous grid
 // (pdl_wait) before their first access to global memory.

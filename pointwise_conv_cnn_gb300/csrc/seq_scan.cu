@@ -6,133 +6,183 @@ namespace fcm {
 namespace seq {
 
 struct TokenArgs {
-    ScanArgs s;
-    int lpc;      // lanes per channel, a power of two, 4 * lpc >= n
-    int chunks;   // times a thread takes U sequences
+    Seqs q;
+    const void *x, *dt, *bm, *cm, *z;
+    const float *a, *skip, *dt_bias, *state_in;
+    void *y;
+    float *state_out;
+    int ld_x, ld_dt, ld_b, ld_c, ld_z, ld_y;
+    int c, n, cpg, softplus;
+    int blocks;   // of channels
+    int turns;    // blocks per block of channels: each takes every turns-th pair of sequences
 };
 
-// Sequences of at most one row.  A thread has four states of one channel and takes U sequences at
-// a time: it reads all that they need before it writes anything.  VEC: the states, a, bm and cm
-// are read four at a time.
-template <typename T, bool VEC, int U>
-__global__ void __launch_bounds__(128) scan_token_kernel(const TokenArgs ta) {
-    const ScanArgs &a = ta.s;
+// p's row of `ld` elements: one 32 x 32 bit product.
+template <typename T> __device__ __forceinline__ const T *row_of(const void *p, int row, int ld) {
+    return static_cast<const T *>(p) + (long long)row * ld;
+}
+
+// Sequences of at most one row: what counts is the states' way through the chip and back.  A thread
+// has four states of one channel (LPC lanes have all n), of two sequences at a time; its block goes
+// from pair to pair, and a pair's states, B, C, x, dt and z are loaded while the pair before is
+// computed (the slots that say where, one pair earlier).  Loads are unconditional, so that they are
+// all under way at once: what does not exist is read from a place that does, and not used.  The
+// steps and gates are made once per channel, by the block's threads together.  VEC: the states, a,
+// bm and cm are read, and the states written, four at a time.
+template <typename T, bool VEC, int LPC>
+__global__ void __launch_bounds__(128, 6) scan_token_kernel(const TokenArgs a) {
+    constexpr int U = 2, CHANS = 128 / LPC;
+    __shared__ float4 prep[2][U * CHANS];   // step, step * x, skip * x, gate of [sequence][channel]
     tc::pdl_wait();
     tc::pdl_launch_dependents();
-    const int lpc = ta.lpc, part = threadIdx.x % lpc, n0 = 4 * part;
-    const int d = blockIdx.x * (128 / lpc) + threadIdx.x / lpc;
-    const bool live = d < a.c;
-    const int dd = live ? d : 0, g = dd / a.cpg;
-    bool in[4];
-    float av[4];
+    const int n0 = 4 * (threadIdx.x % LPC), ch = threadIdx.x / LPC;
+    const int d0 = (int)(blockIdx.x % a.blocks) * CHANS, d = min(d0 + ch, a.c - 1);
+    const bool live = d0 + ch < a.c, some = a.q.tokens > 0, mine = VEC ? n0 < a.n : true;
+    const int last = (int)a.q.tokens - 1;
+    // the sequence and channel whose step this thread makes
+    const int pu = min((int)threadIdx.x / CHANS, U - 1), pd = min(d0 + (int)threadIdx.x % CHANS, a.c - 1);
+    const bool makes = (int)threadIdx.x < U * CHANS;
+    const float bias = a.dt_bias ? a.dt_bias[pd] : 0.0f, skip = a.skip ? a.skip[pd] : 0.0f;
+
+    // four elements from n0 on (p: of the state that is read first), or the last one in the place
+    // of those past n
+    const int nl = VEC ? min(n0, a.n - 4) : min(n0, a.n - 1);
+    auto four = [&](auto &to, const auto *p) {
+        typedef typename std::remove_const<typename std::remove_pointer<decltype(p)>::type>::type E;
+        if (VEC) {
+            to = *reinterpret_cast<const Vec<E, 4> *>(p);
+        } else {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        in[i] = live && (VEC ? n0 < a.n : n0 + i < a.n);
-        av[i] = in[i] ? a.a[(size_t)dd * a.n + n0 + i] * kLog2e : 0.0f;
-    }
-    const float bias = a.dt_bias ? a.dt_bias[dd] : 0.0f, skip = a.skip ? a.skip[dd] : 0.0f;
-    for (int chunk = 0; chunk < ta.chunks; chunk++) {
-        const int q0 = (blockIdx.y * ta.chunks + chunk) * U;
-        if (q0 >= a.q.n_seq) break;
-        float h[U][4], b[U][4], c[U][4], x[U], dt[U], z[U];
-        long long t[U];
-        int len[U], row[U];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            len[u] = 0, row[u] = -1, t[u] = 0;
-            x[u] = dt[u] = z[u] = 0.0f;
-            if (q0 + u < a.q.n_seq) {
-                seq_rows(a.q, q0 + u, t[u], len[u]);
-                if (a.state_in || a.state_out) row[u] = state_row(a.q, q0 + u);
-            }
-            const float *hp = a.state_in + ((size_t)(row[u] < 0 ? 0 : row[u]) * a.c + dd) * a.n + n0;
-            const T *bp = static_cast<const T *>(a.bm) + t[u] * a.ld_b + (long long)g * a.n + n0;
-            const T *cp = static_cast<const T *>(a.cm) + t[u] * a.ld_c + (long long)g * a.n + n0;
-            const bool some = len[u] > 0 && live;
-#pragma unroll
-            for (int i = 0; i < 4; i++) h[u][i] = b[u][i] = c[u][i] = 0.0f;
-            if (VEC) {
-                if (in[0] && row[u] >= 0 && a.state_in) {
-                    const float4 v = *reinterpret_cast<const float4 *>(hp);
-                    h[u][0] = v.x, h[u][1] = v.y, h[u][2] = v.z, h[u][3] = v.w;
-                }
-                if (in[0] && some) {
-                    reinterpret_cast<const Vec<T, 4> *>(bp)->get(b[u]);
-                    reinterpret_cast<const Vec<T, 4> *>(cp)->get(c[u]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if (in[i] && row[u] >= 0 && a.state_in) h[u][i] = hp[i];
-                    if (in[i] && some) {
-                        b[u][i] = Storage<T>::to_f(bp[i]);
-                        c[u][i] = Storage<T>::to_f(cp[i]);
-                    }
-                }
-            }
-            if (some) {
-                x[u] = Storage<T>::to_f(static_cast<const T *>(a.x)[t[u] * a.ld_x + d]);
-                dt[u] = Storage<T>::to_f(static_cast<const T *>(a.dt)[t[u] * a.ld_dt + d]);
-                if (a.z) z[u] = Storage<T>::to_f(static_cast<const T *>(a.z)[t[u] * a.ld_z + d]);
-            }
+            for (int i = 0; i < 4; i++) to.e[i] = p[min(i, a.n - 1 - nl)];
         }
+    };
+    const int cn = a.c * a.n, gn = d / a.cpg * a.n + nl;
+    const float *state_in = a.state_in + (size_t)d * a.n + nl;
+    float *state_out = a.state_out + (size_t)d * a.n + n0;
+    const T *bm = static_cast<const T *>(a.bm) + gn, *cm = static_cast<const T *>(a.cm) + gn;
+    T *y = static_cast<T *>(a.y) + d;
+    Vec<float, 4> av;
+    four(av, a.a + (size_t)d * a.n + nl);
+#pragma unroll
+    for (int i = 0; i < 4; i++) av.e[i] *= kLog2e;
+
+    struct Where {
+        int t[U], len[U], row[U];   // len -1: there is no such sequence
+    };
+    auto look = [&](int q0) {
+        Where w;
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            float step = dt[u] + bias;
-            if (a.softplus) {
-                float unused = 0.0f;
-                softplus2(step, unused);
+            const int q = min(q0 + u, a.q.n_seq - 1);
+            long long t;
+            seq_rows(a.q, q, t, w.len[u]);
+            w.t[u] = min((int)t, last);
+            if (q0 + u >= a.q.n_seq) w.len[u] = -1;
+            w.row[u] = a.state_in || a.state_out ? state_row(a.q, q) : -1;
+        }
+        return w;
+    };
+    struct Loads {
+        Vec<float, 4> h[U];
+        Vec<T, 4> b[U], c[U];
+        T x, dt, z;
+    };
+    auto load = [&](const Where &w, Loads &v) {
+        if (a.state_in) {
+#pragma unroll
+            for (int u = 0; u < U; u++) four(v.h[u], row_of<float>(state_in, max(w.row[u], 0), cn));
+        }
+        if (some) {
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                four(v.b[u], row_of<T>(bm, w.t[u], a.ld_b));
+                four(v.c[u], row_of<T>(cm, w.t[u], a.ld_c));
             }
-            const float du = step * x[u];
-            float o = 0.0f;
-            if (len[u] > 0) {
+            const int at = pu ? w.t[1] : w.t[0];
+            v.x = row_of<T>(a.x, at, a.ld_x)[pd];
+            v.dt = row_of<T>(a.dt, at, a.ld_dt)[pd];
+            if (a.z) v.z = row_of<T>(a.z, at, a.ld_z)[pd];
+        }
+    };
+    const int stride = U * a.turns;
+    int q0 = (int)(blockIdx.x / a.blocks) * U;
+    Where where = look(q0), then = look(q0 + stride);
+    Loads now, next;
+    load(where, now);
+    for (int turn = 0; q0 < a.q.n_seq; q0 += stride, turn ^= 1) {
+        if (q0 + stride < a.q.n_seq) load(then, next);
+        const Where after = look(q0 + 2 * stride);
+        if (makes && some) {
+            const float x = Storage<T>::to_f(now.x);
+            float step = Storage<T>::to_f(now.dt) + bias, unused = 0.0f;
+            if (a.softplus) softplus2(step, unused);
+            prep[turn][threadIdx.x] = make_float4(step, step * x, a.skip ? skip * x : 0.0f,
+                                                  a.z ? silu(Storage<T>::to_f(now.z)) : 1.0f);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            Vec<float, 4> h = now.h[u];
+            if (!a.state_in || where.row[u] < 0)
+#pragma unroll
+                for (int i = 0; i < 4; i++) h.e[i] = 0.0f;
+            if (where.len[u] > 0) {
+                const float4 p = prep[turn][u * CHANS + ch];
+                float bv[4], cv[4], o = 0.0f;
+                now.b[u].get(bv);
+                now.c[u].get(cv);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    if (!in[i]) continue;   // a padding state's 0 * infinity stays out of the sum
-                    h[u][i] = fmaf(ex2(step * av[i]), h[u][i], du * b[u][i]);
-                    o = fmaf(c[u][i], h[u][i], o);
+                    h.e[i] = fmaf(ex2(p.x * av.e[i]), h.e[i], p.y * bv[i]);
+                    if (VEC || n0 + i < a.n) o = fmaf(cv[i], h.e[i], o);
                 }
+                o = mine ? o : 0.0f;
+#pragma unroll
+                for (int m = 1; m < LPC; m *= 2) o += __shfl_xor_sync(0xFFFFFFFFu, o, m);
+                if (n0 == 0 && live) y[(long long)where.t[u] * a.ld_y] = Storage<T>::from_f((o + p.z) * p.w);
             }
-            for (int m = 1; m < lpc; m *= 2) o += __shfl_xor_sync(0xFFFFFFFFu, o, m);
-            if (part == 0 && live && len[u] > 0) {
-                if (a.skip) o = fmaf(skip, x[u], o);
-                if (a.z) o *= silu(z[u]);
-                static_cast<T *>(a.y)[t[u] * a.ld_y + d] = Storage<T>::from_f(o);
-            }
-            if (row[u] >= 0 && a.state_out) {
-                float *hp = a.state_out + ((size_t)row[u] * a.c + dd) * a.n + n0;
+            if (where.len[u] >= 0 && where.row[u] >= 0 && a.state_out && live) {
+                float *to = state_out + (long long)where.row[u] * cn;
                 if (VEC) {
-                    if (in[0]) *reinterpret_cast<float4 *>(hp) = make_float4(h[u][0], h[u][1], h[u][2], h[u][3]);
+                    if (mine) *reinterpret_cast<Vec<float, 4> *>(to) = h;
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        if (in[i]) hp[i] = h[u][i];
+                        if (n0 + i < a.n) to[i] = h.e[i];
                 }
             }
         }
+        now = next, where = then, then = after;
     }
+}
+
+template <typename T, int LPC>
+static cudaError_t launch_tokens(TokenArgs t, int sms, bool vec, cudaStream_t st) {
+    constexpr int CHANS = 128 / LPC;
+    t.blocks = (t.c + CHANS - 1) / CHANS;
+    // a few blocks for each place an SM has, or as many as there are pairs
+    const long long pairs = (t.q.n_seq + 1) / 2, room = (long long)sms * 12 / t.blocks;
+    t.turns = (int)(pairs < room ? pairs : room > 1 ? room : 1);
+    const long long grid = (long long)t.blocks * t.turns;
+    if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+    return launch(vec ? scan_token_kernel<T, true, LPC> : scan_token_kernel<T, false, LPC>, dim3((unsigned)grid),
+                  128, 0, st, t);
 }
 
 template <typename T>
 static cudaError_t run_tokens(const ScanArgs &a, int sms, cudaStream_t st) {
-    TokenArgs t = {a, 1, 1};
-    while (4 * t.lpc < a.n) t.lpc *= 2;
+    const TokenArgs t = {a.q, a.x, a.dt, a.bm, a.cm, a.z, a.a, a.skip, a.dt_bias, a.state_in, a.y, a.state_out,
+                         (int)a.ld_x, (int)a.ld_dt, (int)a.ld_b, (int)a.ld_c, (int)a.ld_z, (int)a.ld_y,
+                         a.c, a.n, a.cpg, a.softplus, 0, 0};
     const size_t four = 4 * sizeof(T);
-    const bool vec = a.n % 4 == 0 && aligned16(a.state_in) && aligned16(a.state_out) &&
+    const bool vec = a.n % 4 == 0 && aligned16(a.a) && aligned16(a.state_in) && aligned16(a.state_out) &&
                      reinterpret_cast<uintptr_t>(a.bm) % four == 0 && reinterpret_cast<uintptr_t>(a.cm) % four == 0 &&
                      a.ld_b % 4 == 0 && a.ld_c % 4 == 0;
-    const unsigned gx = (unsigned)((a.c + 128 / t.lpc - 1) / (128 / t.lpc));
-    const bool many = (long long)gx * a.q.n_seq >= (long long)sms * 64;
-    const int u = many ? 4 : 1;
-    t.chunks = many ? 2 : 1;
-    const long long gy = (a.q.n_seq + (long long)u * t.chunks - 1) / (u * t.chunks);
-    if (gy > 65535) {
-        t.chunks = (int)((a.q.n_seq + 65535LL * u - 1) / (65535LL * u));
-    }
-    const unsigned gyy = (unsigned)((a.q.n_seq + (long long)u * t.chunks - 1) / ((long long)u * t.chunks));
-    void (*kernel)(TokenArgs) = vec ? (many ? scan_token_kernel<T, true, 4> : scan_token_kernel<T, true, 1>)
-                                    : (many ? scan_token_kernel<T, false, 4> : scan_token_kernel<T, false, 1>);
-    return launch(kernel, dim3(gx, gyy), 128, 0, st, t);
+    if (a.n <= 8) return launch_tokens<T, 2>(t, sms, vec, st);
+    if (a.n <= 16) return launch_tokens<T, 4>(t, sms, vec, st);
+    if (a.n <= 32) return launch_tokens<T, 8>(t, sms, vec, st);
+    if (a.n <= 64) return launch_tokens<T, 16>(t, sms, vec, st);
+    return launch_tokens<T, 32>(t, sms, vec, st);
 }
 
 // Which shape scans, and over how many parts a sequence is split.  More states per thread cost
@@ -201,6 +251,8 @@ extern "C" fcm_status fcm_selective_scan(const fcm_scan_desc *desc, const void *
         return fcm_fail(FCM_ERR_INVALID_ARG, "c %d, n_state %d", d.c, d.n_state);
     if (d.n_state > seq::kMaxState)
         return fcm_fail(FCM_ERR_UNSUPPORTED, "n_state %d above %d", d.n_state, seq::kMaxState);
+    if ((long long)d.c * d.n_state > 0x7FFFFFFFLL)
+        return fcm_fail(FCM_ERR_UNSUPPORTED, "c * n_state above 2^31 - 1");
     if (d.groups < 1 || d.c % d.groups)
         return fcm_fail(FCM_ERR_INVALID_ARG, "%d groups do not divide %d channels", d.groups, d.c);
     if (d.dtype < FCM_F32 || d.dtype > FCM_BF16)

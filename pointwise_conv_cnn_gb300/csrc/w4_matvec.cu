@@ -20,26 +20,39 @@ struct W4Args {
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (std::is_same<T, __half>::value)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 16 bytes, or zeros; a predicate instead of a branch, behind which nothing could be under way.
+__device__ __forceinline__ uint4 load_if(const void *p, bool yes) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"((int)yes));
+    return v;
+}
+
 // The values of bits [4j, 4j + 4) and [4j + 16, 4j + 20) of q, less 8, in two halves: the bits are
-// put into the mantissa of 1024 (f16) or 128 (bf16), whose last place is 1 there, so the
-// difference is exact.
+// put into the mantissa of 1024 (f16) or 128 (bf16), so that the difference is exact.  f16's
+// mantissa has room for them four places up as well, which saves shifts: 1024 + 16 q is scaled back.
 template <typename T> __device__ __forceinline__ uint32_t two_weights(uint32_t q, int j) {
-    const uint32_t bits = (q >> (4 * j)) & 0x000F000Fu;
     uint32_t r;
     if constexpr (std::is_same<T, __half>::value) {
-        const uint32_t v = bits | 0x64006400u, o = 0x64086408u;   // 1024 + q, 1032
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(o));
+        const uint32_t s = j >= 2 ? q >> 8 : q;
+        if (j % 2 == 0) {
+            const uint32_t v = (s & 0x000F000Fu) | 0x64006400u, o = 0x64086408u;   // 1024 + q, 1032
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(o));
+        } else {
+            const uint32_t v = (s & 0x00F000F0u) | 0x64006400u, k = 0x2C002C00u, o = 0xD480D480u;   // 1/16, -72
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(k), "r"(o));
+        }
     } else {
-        const uint32_t v = bits | 0x43004300u, o = 0x43084308u;   // 128 + q, 136
+        const uint32_t v = ((q >> (4 * j)) & 0x000F000Fu) | 0x43004300u, o = 0x43084308u;   // 128 + q, 136
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(o));
     }
     return r;
@@ -53,9 +66,9 @@ template <typename T> __device__ __forceinline__ uint32_t two_weights(uint32_t q
 // from memory to the tensor cores as whole numbers, without a detour, and a group's sum is
 // scaled in 32 bits.  XV: x's rows are 16-byte aligned.
 template <typename T, int G, int NT, bool XV>
-__global__ void __launch_bounds__(512) w4_kernel(const W4Args a) {
+__global__ void __launch_bounds__(512, NT == 1 && G >= 64 ? 2 : 1) w4_kernel(const W4Args a) {
     constexpr int WORDS = G / 32;   // words per lane and group
-    constexpr int UB = 128 / G * 4; // groups loaded at once: 64 bytes of each row... of each lane
+    constexpr int UB = 128 / G;     // groups loaded at once
     extern __shared__ float red[];
     tc::pdl_wait();
     tc::pdl_launch_dependents();
@@ -66,58 +79,67 @@ __global__ void __launch_bounds__(512) w4_kernel(const W4Args a) {
     const uint8_t *wa = static_cast<const uint8_t *>(a.qw) + (size_t)oa * (a.in / 2) + t * (G / 8);
     const uint8_t *wb = static_cast<const uint8_t *>(a.qw) + (size_t)ob * (a.in / 2) + t * (G / 8);
     const T *sa = static_cast<const T *>(a.qs) + (size_t)oa * a.units, *sb = static_cast<const T *>(a.qs) + (size_t)ob * a.units;
+    // A column of the product is a token's alone.  Where there are fewer tokens, its inputs are not
+    // read (the lanes of one token alone take a quarter of the cache's bandwidth that all take).
     const T *x[NT];
     bool token[NT];
 #pragma unroll
     for (int i = 0; i < NT; i++) {
         token[i] = m0 + i * 8 + r < a.m;
-        x[i] = static_cast<const T *>(a.x) + (long long)(token[i] ? m0 + i * 8 + r : m0) * a.ld_x + t * (G / 4);
+        x[i] = static_cast<const T *>(a.x) + (long long)min(m0 + i * 8 + r, a.m - 1) * a.ld_x + t * (G / 4);
     }
     float sum[NT][4] = {};
     struct alignas(4 * WORDS) Words {
         uint32_t w[WORDS];
     };
-    auto group = [&](int u, const Words &qa, const Words &qb, float fa, float fb, bool in) {
-        float c[NT][4] = {};
+    struct Inputs {
+        uint4 v[NT][WORDS];
+    };
+    auto inputs = [&](int u) {
+        Inputs in;
 #pragma unroll
-        for (int w = 0; w < WORDS; w++) {
-            uint32_t b[NT][4];
+        for (int i = 0; i < NT; i++)
 #pragma unroll
-            for (int i = 0; i < NT; i++) {
+            for (int w = 0; w < WORDS; w++) {
                 const T *p = x[i] + (size_t)u * G + w * 8;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (token[i] && in) {
-                    if (XV) {
-                        v = *reinterpret_cast<const uint4 *>(p);
-                    } else {
-                        const unsigned short *e = reinterpret_cast<const unsigned short *>(p);
-                        v = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                                       e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
-                    }
+                if (XV) {
+                    in.v[i][w] = load_if(p, token[i]);
+                } else {
+                    const unsigned short *e = reinterpret_cast<const unsigned short *>(p);
+                    in.v[i][w] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                            e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
                 }
-                b[i][0] = __byte_perm(v.x, v.z, 0x5410), b[i][1] = __byte_perm(v.x, v.z, 0x7632);
-                b[i][2] = __byte_perm(v.y, v.w, 0x5410), b[i][3] = __byte_perm(v.y, v.w, 0x7632);
             }
+        return in;
+    };
+    auto group = [&](const Inputs &in, const Words &qa, const Words &qb, float fa, float fb) {
+        constexpr int SUMS = WORDS >= 4 ? 2 : 1;   // a long group's products need not wait for each other
+        float c[SUMS][NT][4] = {};
+#pragma unroll
+        for (int w = 0; w < WORDS; w++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const uint32_t f[4] = {two_weights<T>(qa.w[w], 2 * h), two_weights<T>(qb.w[w], 2 * h),
                                        two_weights<T>(qa.w[w], 2 * h + 1), two_weights<T>(qb.w[w], 2 * h + 1)};
 #pragma unroll
-                for (int i = 0; i < NT; i++) mma16816<T>(c[i], f, b[i][2 * h], b[i][2 * h + 1]);
+                for (int i = 0; i < NT; i++) {
+                    const uint4 v = in.v[i][w];
+                    const uint32_t lo = h ? v.y : v.x, hi = h ? v.w : v.z;
+                    mma16816<T>(c[h % SUMS][i], f, __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+                }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-            sum[i][0] = fmaf(c[i][0], fa, sum[i][0]);
-            sum[i][1] = fmaf(c[i][1], fa, sum[i][1]);
-            sum[i][2] = fmaf(c[i][2], fb, sum[i][2]);
-            sum[i][3] = fmaf(c[i][3], fb, sum[i][3]);
-        }
+        for (int i = 0; i < NT; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float v = SUMS == 2 ? c[0][i][j] + c[SUMS - 1][i][j] : c[0][i][j];
+                sum[i][j] = fmaf(v, j < 2 ? fa : fb, sum[i][j]);
+            }
     };
-    const int whole = a.in / G;   // groups that are not short
-    const int per = (a.units + warps - 1) / warps, u0 = warp * per, u1 = min(a.units, u0 + per);
+    const int per = (a.units + warps * UB - 1) / (warps * UB) * UB, u0 = min(a.units, warp * per), u1 = min(a.units, u0 + per);
+    const int whole = min(u1, a.in / G);   // the last group may be short
     int u = u0;
-    for (; u + UB <= min(u1, whole); u += UB) {
+    for (; u + UB <= whole; u += UB) {
         Words qa[UB], qb[UB];
         float fa[UB], fb[UB];
 #pragma unroll
@@ -128,16 +150,18 @@ __global__ void __launch_bounds__(512) w4_kernel(const W4Args a) {
             fb[i] = Storage<T>::to_f(sb[u + i]);
         }
 #pragma unroll
-        for (int i = 0; i < UB; i++) group(u + i, qa[i], qb[i], fa[i], fb[i], true);
+        for (int i = 0; i < UB; i++) group(inputs(u + i), qa[i], qb[i], fa[i], fb[i]);
     }
     for (; u < u1; u++) {
         const bool in = u * G + t * (G / 4) < a.in;   // a short group ends with a lane's quarter
         Words qa = {}, qb = {};
+        Inputs v = {};                                // whose inputs past the end are zeros
         if (in) {
             qa = *reinterpret_cast<const Words *>(wa + (size_t)u * (G / 2));
             qb = *reinterpret_cast<const Words *>(wb + (size_t)u * (G / 2));
+            v = inputs(u);
         }
-        group(u, qa, qb, Storage<T>::to_f(sa[u]), Storage<T>::to_f(sb[u]), in);
+        group(v, qa, qb, Storage<T>::to_f(sa[u]), Storage<T>::to_f(sb[u]));
     }
     // the warps' sums, in their order
 #pragma unroll
