@@ -12,8 +12,8 @@ the layers over sequences.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
-import struct
 import threading
 
 __all__ = [
@@ -35,7 +35,6 @@ LIB_PATH = os.path.join(_HERE, "libfcm.so")
 
 FCM_OK = 0
 FCM_ERR_INVALID_ARG = 1
-FCM_ERR_UNSUPPORTED = 2
 STATUS_NAMES = {0: "FCM_OK", 1: "FCM_ERR_INVALID_ARG", 2: "FCM_ERR_UNSUPPORTED",
                 3: "FCM_ERR_ALIGNMENT", 4: "FCM_ERR_SMEM_BUDGET", 5: "FCM_ERR_CUDA",
                 6: "FCM_ERR_TIMEOUT", 7: "FCM_ERR_DEVICE_FAULT", 8: "FCM_ERR_NO_DEVICE"}
@@ -443,118 +442,27 @@ class FusedConvModule:
             pass
 
 
-# ---- Layers over sequences (tensors in, tensors out; include/fcm.h has the definitions).
-# A single token's kernel takes a few microseconds, so these calls keep their own cost low: the
-# descriptors are packed into bytes laid out as the C structs (tests compare them with the
-# ctypes mirrors above).
-_CONV_DESC = struct.Struct("qiii4xPPiiiiqq")
-_SCAN_DESC = struct.Struct("qiii4xPPiiiii4xqqqqqq")
-_W4_DESC = struct.Struct("iiiiiiqq")
-_torch = None
-_code = {}         # torch dtype -> fcm_dtype
+# ---- Layers over sequences, on tensors (include/fcm.h has the definitions).  The calls' arguments are
+# checked and passed on by _tensor_calls (csrc/tensor_calls.cpp): a single token's kernel takes two
+# or three microseconds, and checking a dozen tensors here would take ten.
+_calls = None
 
 
-def _bind_torch():
-    """torch is imported on the first call that takes tensors, as elsewhere in this binding."""
-    global _torch
-    import torch
-    _code.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    _torch = torch
-    return torch
-
-
-def _refuse(message: str):
-    raise FcmError(FCM_ERR_INVALID_ARG, message)
-
-
-def _dtype_code(x) -> int:
-    if _torch is None:
-        _bind_torch()
-    code = _code.get(x.dtype)
-    if code is None:
-        raise FcmError(FCM_ERR_UNSUPPORTED, f"x is {x.dtype}: float32, float16, bfloat16 are supported")
-    return code
-
-
-def _stream_of(x, stream) -> int:
-    """The raw stream handle; x must lie on the current device."""
-    dev = x.get_device()
-    if dev < 0 or dev != _torch._C._cuda_getDevice():
-        _refuse("x must be a CUDA tensor on the current device")
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(dev)
-    return getattr(stream, "cuda_stream", stream)
-
-
-def _ptr(t, like, dtype, shape, what) -> int:
-    """Address of a contiguous tensor of this dtype and shape on `like`'s device (0: None)."""
-    if t is None:
-        return 0
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != like.get_device() \
-            or not t.is_contiguous():
-        _refuse(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on x's device, "
-                f"not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
-
-
-def _distance(lead, c, stride, what) -> int:
-    """Row distance of rows [*lead] of c elements whose leading dimensions have these strides."""
-    if 0 in lead:
-        return c
-    if lead[-1] > 1:
-        ld = stride[len(lead) - 1]
-        if len(lead) == 2 and lead[0] > 1 and stride[0] != lead[1] * ld:
-            _refuse(f"{what}: rows must all be the same distance apart, strides {stride}")
-    else:
-        ld = stride[0] if lead[0] > 1 else c
-    if ld < c:
-        _refuse(f"{what}: rows overlap, strides {stride}")
-    return ld
-
-
-def _rows(t, like, lead, c, what) -> int:
-    """Row distance of activations [*lead, c]: `like`'s dtype and device, each row's elements
-    together, all rows the same distance apart."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not like.dtype or t.get_device() != like.get_device() or shape != (*lead, c):
-        _refuse(f"{what} must be a {like.dtype} tensor of shape {(*lead, c)} on x's device, not "
-                f"{t.dtype} {tuple(shape)} on {t.device}")
-    if stride[-1] != 1 and c > 1 and 0 not in lead:
-        _refuse(f"{what}: a row's elements must lie together, strides {stride}")
-    return _distance(lead, c, stride, what)
-
-
-def _group_rows(t, like, lead, groups, n, what) -> int:
-    """The same of [*lead, groups, n], whose groups lie side by side in a row."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not like.dtype or t.get_device() != like.get_device() \
-            or shape != (*lead, groups, n):
-        _refuse(f"{what} must be a {like.dtype} tensor of shape {(*lead, groups, n)} on x's device, "
-                f"not {t.dtype} {tuple(shape)} on {t.device}")
-    if (stride[-1] != 1 and n > 1 or stride[-2] != n and groups > 1) and 0 not in lead:
-        _refuse(f"{what}: a row's groups must lie side by side, strides {stride}")
-    return _distance(lead, groups * n, stride, what)
-
-
-def _sequences(x, seq_start, max_len, slot):
-    """(leading shape, tokens, sequences, longest, seq_start's address, slot's address) of x
-    [sequences, length, c], or [tokens, c] with seq_start."""
-    shape = x.shape
-    if seq_start is None:
-        if len(shape) != 3:
-            _refuse("x must be [sequences, length, channels], or [tokens, channels] with seq_start")
-        n_seq, longest = shape[0], shape[1]
-        tokens, start = n_seq * longest, 0
-    else:
-        if len(shape) != 2:
-            _refuse("x must be [tokens, channels] with seq_start")
-        tokens, n_seq = shape[0], len(seq_start) - 1
-        longest = tokens if max_len is None else max_len
-        if n_seq < 0:
-            _refuse("seq_start must have one element more than there are sequences")
-        start = _ptr(seq_start, x, _torch.int32, (n_seq + 1,), "seq_start")
-    return (shape[:-1], tokens, n_seq, longest, start,
-            0 if slot is None else _ptr(slot, x, _torch.int32, (n_seq,), "slot"))
+def _bind_calls():
+    """Load the marshalling module, on the first call that takes tensors.  Raises if it is missing:
+    there is no other way to make these calls."""
+    global _calls
+    lib = load_library()
+    import torch  # noqa: F401  (whose libraries the module uses)
+    try:
+        module = importlib.import_module("._tensor_calls", __name__)
+    except ImportError as e:
+        raise FileNotFoundError(f"{os.path.join(_HERE, '_tensor_calls.so')} does not load ({e}): build it "
+                                "with `python -m pointwise_conv_cnn_gb300.build`") from e
+    module.bind(FcmError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+        "fcm_causal_conv", "fcm_selective_scan", "fcm_w4_matvec", "fcm_last_error")))
+    _calls = module
+    return module
 
 
 def causal_conv(x, w, y, scale=None, bias=None, act: str = "silu", seq_start=None, max_len=None,
@@ -567,26 +475,8 @@ def causal_conv(x, w, y, scale=None, bias=None, act: str = "silu", seq_start=Non
     state_in, state_out: [slots, ksize - 1, c] in x's dtype, the rows before and after (the same
     tensor updates it in place); slot: int32 [sequences], their rows.  max_len: an upper bound
     of the lengths under seq_start (default: all tokens)."""
-    code = _dtype_code(x)
-    lead, tokens, n_seq, longest, start, slot_p = _sequences(x, seq_start, max_len, slot)
-    c = x.shape[-1]
-    if w.dim() != 2:
-        _refuse("w must be [channels, ksize]")
-    k, f32, slots = w.shape[1], _torch.float32, 0
-    some = state_in if state_in is not None else state_out
-    if some is not None:
-        slots = some.shape[0]
-    if act not in ACTS:
-        _refuse(f"activation {act!r}")
-    desc = _CONV_DESC.pack(tokens, n_seq, longest, slots, start, slot_p, c, k, code, ACTS[act],
-                           _rows(x, x, lead, c, "x"), _rows(y, x, lead, c, "y"))
-    state = (slots, k - 1, c)
-    status = (_lib or load_library()).fcm_causal_conv(
-        desc, x.data_ptr(), _ptr(w, x, x.dtype, (c, k), "w"), _ptr(scale, x, f32, (c,), "scale"),
-        _ptr(bias, x, f32, (c,), "bias"), _ptr(state_in, x, x.dtype, state, "state_in"),
-        y.data_ptr(), _ptr(state_out, x, x.dtype, state, "state_out"), _stream_of(x, stream))
-    if status:
-        _check(status)
+    (_calls or _bind_calls()).causal_conv(
+        x, w, y, scale, bias, act, seq_start, max_len, slot, state_in, state_out, stream)
 
 
 def selective_scan(x, dt, a, b, c, y, skip=None, z=None, dt_bias=None, softplus: bool = True,
@@ -598,34 +488,9 @@ def selective_scan(x, dt, a, b, c, y, skip=None, z=None, dt_bias=None, softplus:
     shape with [groups, n] or [n] behind it; all in x's dtype, rows may be column blocks of wider
     tensors.  a: float32 [ch, n]; skip, dt_bias: float32 [ch].  state_in, state_out: float32
     [slots, ch, n]; seq_start, max_len, slot as for causal_conv."""
-    code = _dtype_code(x)
-    lead, tokens, n_seq, longest, start, slot_p = _sequences(x, seq_start, max_len, slot)
-    ch, f32 = x.shape[-1], _torch.float32
-    if a.dim() != 2:
-        _refuse("a must be [channels, states]")
-    n = a.shape[1]
-    slots = 0
-    some = state_in if state_in is not None else state_out
-    if some is not None:
-        slots = some.shape[0]
-    if b.dim() == len(lead) + 2:
-        groups = b.shape[-2]
-        ld_b, ld_c = (_group_rows(t, x, lead, groups, n, what) for t, what in ((b, "b"), (c, "c")))
-    else:
-        groups, ld_b, ld_c = 1, _rows(b, x, lead, n, "b"), _rows(c, x, lead, n, "c")
-    desc = _SCAN_DESC.pack(tokens, n_seq, longest, slots, start, slot_p, ch, n, groups, code,
-                           1 if softplus else 0, _rows(x, x, lead, ch, "x"),
-                           _rows(dt, x, lead, ch, "dt"), ld_b, ld_c,
-                           0 if z is None else _rows(z, x, lead, ch, "z"),
-                           _rows(y, x, lead, ch, "y"))
-    state = (slots, ch, n)
-    status = (_lib or load_library()).fcm_selective_scan(
-        desc, x.data_ptr(), dt.data_ptr(), _ptr(a, x, f32, (ch, n), "a"), b.data_ptr(),
-        c.data_ptr(), _ptr(skip, x, f32, (ch,), "skip"), 0 if z is None else z.data_ptr(),
-        _ptr(dt_bias, x, f32, (ch,), "dt_bias"), _ptr(state_in, x, f32, state, "state_in"),
-        y.data_ptr(), _ptr(state_out, x, f32, state, "state_out"), _stream_of(x, stream))
-    if status:
-        _check(status)
+    (_calls or _bind_calls()).selective_scan(
+        x, dt, a, b, c, y, skip, z, dt_bias, softplus, seq_start, max_len, slot, state_in, state_out,
+        stream)
 
 
 def w4_matvec(x, qw, qs, y, group: int, scale=None, bias=None, act: str = "none",
@@ -635,22 +500,4 @@ def w4_matvec(x, qw, qs, y, group: int, scale=None, bias=None, act: str = "none"
     x: [m, in], y: [m, out], rows may be column blocks of wider tensors; qw: uint8 [out, in / 2], an
     even input's value in the low four bits, values 0..15 standing for -8..7; qs: [out,
     ceil(in / group)] in x's dtype; scale, bias: float32 [out]."""
-    code = _dtype_code(x)
-    if x.dim() != 2 or qw.dim() != 2:
-        _refuse("x must be [m, in] and qw [out, in / 2]")
-    (m, k), o = x.shape, qw.shape[0]
-    lead, f32 = (m,), _torch.float32
-    if group not in (32, 64, 128):
-        raise FcmError(FCM_ERR_UNSUPPORTED, f"group {group}: 32, 64 and 128 are supported")
-    if k % 32:
-        raise FcmError(FCM_ERR_UNSUPPORTED, f"in {k} is not a multiple of 32")
-    if act not in ACTS:
-        _refuse(f"activation {act!r}")
-    desc = _W4_DESC.pack(m, o, k, group, code, ACTS[act], _rows(x, x, lead, k, "x"),
-                         _rows(y, x, lead, o, "y"))
-    status = (_lib or load_library()).fcm_w4_matvec(
-        desc, x.data_ptr(), _ptr(qw, x, _torch.uint8, (o, k // 2), "qw"),
-        _ptr(qs, x, x.dtype, (o, -(-k // group)), "qs"), _ptr(scale, x, f32, (o,), "scale"),
-        _ptr(bias, x, f32, (o,), "bias"), y.data_ptr(), _stream_of(x, stream))
-    if status:
-        _check(status)
+    (_calls or _bind_calls()).w4_matvec(x, qw, qs, y, group, scale, bias, act, stream)

@@ -64,22 +64,15 @@ def test_w4_reference_by_hand():
 
 
 # ------------------------------------------------------------------------------ the descriptors
-@pytest.mark.parametrize("name,mirror,packer", [
-    ("fcm_seqs", fcm.FcmSeqs, None), ("fcm_causal_conv_desc", fcm.FcmCausalConvDesc, "_CONV_DESC"),
-    ("fcm_scan_desc", fcm.FcmScanDesc, "_SCAN_DESC"), ("fcm_w4_desc", fcm.FcmW4Desc, "_W4_DESC")])
-def test_mirrors_follow_the_header(name, mirror, packer):
+@pytest.mark.parametrize("name,mirror,size", [
+    ("fcm_seqs", fcm.FcmSeqs, 40), ("fcm_causal_conv_desc", fcm.FcmCausalConvDesc, 72),
+    ("fcm_scan_desc", fcm.FcmScanDesc, 112), ("fcm_w4_desc", fcm.FcmW4Desc, 40)])
+def test_mirrors_follow_the_header(name, mirror, size):
     body = re.search(r"typedef struct %s \{(.*?)\} %s;" % (name, name), open(HEADER).read(), re.S).group(1)
     body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
     names = [n for decl in body.split(";") for n in re.findall(r"\*?(\w+)\s*(?:,|$)", decl.strip())]
     assert [f.rstrip("_") for f, _ in mirror._fields_] == names
-    if packer:
-        p = getattr(fcm, packer)
-        assert p.size == ctypes.sizeof(mirror)
-        flat = lambda s: [v for f, t in s._fields_ for v in (  # noqa: E731
-            flat(getattr(s, f)) if issubclass(t, ctypes.Structure) else [getattr(s, f) or 0])]
-        count = len(flat(mirror()))
-        values = list(range(1, count + 1))
-        assert flat(mirror.from_buffer_copy(p.pack(*values))) == values
+    assert ctypes.sizeof(mirror) == size
 
 
 # ------------------------------------------------------------------------------ refusals
