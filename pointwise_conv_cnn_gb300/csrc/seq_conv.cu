@@ -22,15 +22,76 @@ struct ConvArgs {
 
 constexpr int kMaxTaps = 8;
 
+// VEC elements of x or of one tap's weights as the products take them: two 16-bit ones in a register
+// (fma.rn.f32.{f16,bf16} widens both factors), or single ones widened.
+template <typename T, int VEC> struct Lane {
+    static constexpr bool PACKED = sizeof(T) == 2 && VEC > 1;
+    static constexpr int N = PACKED ? VEC / 2 : VEC;
+    typedef typename std::conditional<PACKED, uint32_t, float>::type R;
+    R r[N];
+    struct alignas(VEC * sizeof(T)) Bits {
+        uint32_t u[VEC * sizeof(T) >= 4 ? VEC * sizeof(T) / 4 : 1];
+    };
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VEC == 1) {
+            r[0] = Storage<T>::to_f(*p);
+        } else {
+            const Bits v = *reinterpret_cast<const Bits *>(p);
+#pragma unroll
+            for (int i = 0; i < N; i++) r[i] = from_bits(v.u[i]);
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (VEC == 1) {
+            *p = Storage<T>::from_f(r[0]);
+        } else {
+            Bits v;
+#pragma unroll
+            for (int i = 0; i < N; i++) v.u[i] = to_bits(r[i]);
+            *reinterpret_cast<Bits *>(p) = v;
+        }
+    }
+    static __device__ __forceinline__ R from_bits(uint32_t u) {
+        if constexpr (PACKED) return u;
+        else return __uint_as_float(u);
+    }
+    static __device__ __forceinline__ uint32_t to_bits(R v) {
+        if constexpr (PACKED) return v;
+        else return __float_as_uint(v);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < N; i++) r[i] = 0;
+    }
+    // element v of this lane's channels from a value in memory
+    __device__ __forceinline__ void set(int v, T value) {
+        if constexpr (PACKED) {
+            const uint32_t bits = *reinterpret_cast<const unsigned short *>(&value);
+            r[v / 2] = v % 2 ? (r[v / 2] & 0xFFFFu) | bits << 16 : bits;
+        } else {
+            r[v] = Storage<T>::to_f(value);
+        }
+    }
+    __device__ __forceinline__ void multiply_add(float (&acc)[VEC], const Lane &w) const {
+        if constexpr (PACKED) {
+#pragma unroll
+            for (int i = 0; i < N; i++) tc::Fma16<T>::fma2(acc[2 * i], acc[2 * i + 1], r[i], w.r[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++) acc[i] = fmaf(w.r[i], r[i], acc[i]);
+        }
+    }
+};
+
 // One thread: VEC neighbouring channels (16 bytes, or one), a.rows consecutive rows of one
 // sequence.  The K - 1 rows before them are read again from the neighbour's tile or are the cached
-// ones; from there each row is read once and kept in registers for its K uses.  The thread of a
-// sequence's first rows also replaces the cached rows, which it has read by then, so that
-// state_out may be state_in.
+// ones; from there each row is read once and kept in registers, as stored, for its K uses.  The
+// thread of a sequence's first rows also replaces the cached rows, which it has read by then, so
+// that state_out may be state_in.
 template <typename T, int VEC, int K>
 __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
-    typedef Vec<T, VEC> V;
-    constexpr int H = K - 1, U = 4;   // rows before, rows loaded at once
+    typedef Lane<T, VEC> L;
+    constexpr int H = K - 1, U = 8;   // rows before, rows loaded at once
     tc::pdl_wait();
     tc::pdl_launch_dependents();
     const long long id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -46,8 +107,7 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
     const T *x = static_cast<const T *>(a.x) + d + start * a.ld_x;
     T *y = static_cast<T *>(a.y) + d + start * a.ld_y;
 
-    float win[H + U][VEC];   // rows i - H .. i + U - 1
-    V old[K > 1 ? H : 1];    // the cached rows
+    L win[H + U];   // rows i - H .. i + U - 1
     int row = -1;
     size_t at = 0;
     if (K > 1) {
@@ -56,30 +116,27 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
             at = (size_t)(row < 0 ? 0 : row) * H * a.c + d;
 #pragma unroll
             for (int j = 0; j < H; j++) {
-#pragma unroll
-                for (int v = 0; v < VEC; v++) old[j].e[v] = Storage<T>::from_f(0.0f);
-                if (row >= 0 && a.state_in)
-                    old[j] = *reinterpret_cast<const V *>(static_cast<const T *>(a.state_in) + at + (size_t)j * a.c);
+                win[j].zero();
+                if (row >= 0 && a.state_in) win[j].load(static_cast<const T *>(a.state_in) + at + (size_t)j * a.c);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < H; j++) old[j] = *reinterpret_cast<const V *>(x + (long long)(i0 - H + j) * a.ld_x);
+            for (int j = 0; j < H; j++) win[j].load(x + (long long)(i0 - H + j) * a.ld_x);
         }
-#pragma unroll
-        for (int j = 0; j < H; j++) old[j].get(win[j]);
     }
-    float w[VEC * K], s[VEC], b[VEC];
+    L w[K];
+    float s[VEC], b[VEC];
     {
-        constexpr int PIECE = VEC * K * sizeof(T) % 16 == 0 ? 16 / (int)sizeof(T) : 1;   // w's own order
+        constexpr int PIECE = VEC * K * sizeof(T) % 16 == 0 && VEC > 2 ? 16 / (int)sizeof(T) : 1;   // w's own order
 #pragma unroll
         for (int j = 0; j < VEC * K; j += PIECE) {
             const Vec<T, PIECE> p = *reinterpret_cast<const Vec<T, PIECE> *>(static_cast<const T *>(a.w) + (size_t)d * K + j);
 #pragma unroll
-            for (int v = 0; v < PIECE; v++) w[j + v] = Storage<T>::to_f(p.e[v]);
+            for (int v = 0; v < PIECE; v++) w[(j + v) % K].set((j + v) / K, p.e[v]);
         }
 #pragma unroll
         for (int v = 0; v < VEC; v++) s[v] = 1.0f, b[v] = 0.0f;
-        constexpr int F = VEC % 4 == 0 ? 4 : 1;
+        constexpr int F = VEC % 4 == 0 ? 4 : VEC;
 #pragma unroll
         for (int v = 0; v < VEC; v += F) {
             if (a.s) {
@@ -97,39 +154,28 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
     // The state after: the last H places, of which those before 0 are cached rows.  All are read
     // before any is written.
     if (K > 1 && row >= 0 && a.state_out) {
-        V last[K > 1 ? H : 1];
+        L last[K > 1 ? H : 1];
 #pragma unroll
         for (int j = 0; j < H; j++) {
             const int i = len - H + j;
-            V none;
-#pragma unroll
-            for (int v = 0; v < VEC; v++) none.e[v] = Storage<T>::from_f(0.0f);
-            last[j] = none;
-            const T *from = i >= 0 ? x + (long long)i * a.ld_x
-                                   : static_cast<const T *>(a.state_in) + at + (size_t)(i + H) * a.c;
-            if (i >= 0 || a.state_in) last[j] = *reinterpret_cast<const V *>(from);
+            last[j].zero();
+            if (i >= 0) last[j].load(x + (long long)i * a.ld_x);
+            else if (a.state_in) last[j].load(static_cast<const T *>(a.state_in) + at + (size_t)(i + H) * a.c);
         }
 #pragma unroll
-        for (int j = 0; j < H; j++)
-            *reinterpret_cast<V *>(static_cast<T *>(a.state_out) + at + (size_t)j * a.c) = last[j];
+        for (int j = 0; j < H; j++) last[j].store(static_cast<T *>(a.state_out) + at + (size_t)j * a.c);
     }
-    auto rows = [&](int i, int n) {   // rows i .. i + n - 1, n <= U
-        V in[U];
-#pragma unroll
-        for (int u = 0; u < U; u++)
-            if (u < n) in[u] = *reinterpret_cast<const V *>(x + (long long)(i + u) * a.ld_x);
+    auto compute = [&](int i, int n) {   // rows i .. i + n - 1, loaded
 #pragma unroll
         for (int u = 0; u < U; u++) {
             if (u >= n) break;
-            in[u].get(win[H + u]);
             float o[VEC];
 #pragma unroll
-            for (int v = 0; v < VEC; v++) {
-                float acc = 0.0f;
+            for (int v = 0; v < VEC; v++) o[v] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < K; j++) acc = fmaf(w[v * K + j], win[u + j][v], acc);
-                o[v] = fmaf(s[v], acc, b[v]);
-            }
+            for (int j = 0; j < K; j++) win[u + j].multiply_add(o, w[j]);
+#pragma unroll
+            for (int v = 0; v < VEC; v++) o[v] = fmaf(s[v], o[v], b[v]);
             if (a.act == FCM_ACT_SILU) {
 #pragma unroll
                 for (int v = 0; v < VEC; v++) o[v] = silu(o[v]);
@@ -137,18 +183,27 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
 #pragma unroll
                 for (int v = 0; v < VEC; v++) o[v] = act_apply(o[v], a.act);
             }
-            V out;
+            Vec<T, VEC> out;
             out.put(o);
-            *reinterpret_cast<V *>(y + (long long)(i + u) * a.ld_y) = out;
+            *reinterpret_cast<Vec<T, VEC> *>(y + (long long)(i + u) * a.ld_y) = out;
         }
 #pragma unroll
-        for (int j = 0; j < H; j++)
-#pragma unroll
-            for (int v = 0; v < VEC; v++) win[j][v] = win[U + j][v];
+        for (int j = 0; j < H; j++) win[j] = win[U + j];
     };
     int i = i0;
-    for (; i + U <= i1; i += U) rows(i, U);
-    if (i < i1) rows(i, i1 - i);
+    for (; i + U <= i1; i += U) {
+#pragma unroll
+        for (int u = 0; u < U; u++) win[H + u].load(x + (long long)(i + u) * a.ld_x);
+        compute(i, U);
+    }
+    if (i + 1 < i1) {   // the last one again in the place of rows that there are not: no load waits
+#pragma unroll
+        for (int u = 0; u < U; u++) win[H + u].load(x + (long long)min(i + u, i1 - 1) * a.ld_x);
+        compute(i, i1 - i);
+    } else if (i < i1) {
+        win[H].load(x + (long long)i * a.ld_x);
+        compute(i, 1);
+    }
 }
 
 template <typename T, int VEC>
@@ -168,9 +223,16 @@ static void (*pick_conv(int k))(ConvArgs) {
 template <typename T>
 static cudaError_t run_conv(ConvArgs a, int sms, cudaStream_t st) {
     constexpr int VEC = 16 / (int)sizeof(T);
-    const bool vec = ((a.c | a.ld_x | a.ld_y) % VEC) == 0 && aligned16(a.x) && aligned16(a.w) && aligned16(a.s) &&
-                     aligned16(a.b) && aligned16(a.state_in) && aligned16(a.y) && aligned16(a.state_out);
-    const long long cg = vec ? a.c / VEC : a.c, all = (long long)a.q.n_seq * cg;
+    // 16 bytes a thread where every row allows it, else two channels, else one
+    auto rows_allow = [&](int n) {
+        const size_t bytes = n * sizeof(T);
+        auto fits = [](const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; };
+        return ((a.c | a.ld_x | a.ld_y) % n) == 0 && fits(a.x, bytes) && fits(a.y, bytes) && fits(a.state_in, bytes) &&
+               fits(a.state_out, bytes) && fits(a.w, n > 2 ? 16 : sizeof(T)) && fits(a.s, n > 2 ? 16 : 8) &&
+               fits(a.b, n > 2 ? 16 : 8);
+    };
+    const int vec = rows_allow(VEC) ? VEC : rows_allow(2) ? 2 : 1;
+    const long long cg = a.c / vec, all = (long long)a.q.n_seq * cg;
     // no fewer rows than cached ones: only the first tile's window reaches those
     const int least = a.k > 5 ? 8 : 4;
     a.rows = 32;
@@ -179,7 +241,7 @@ static cudaError_t run_conv(ConvArgs a, int sms, cudaStream_t st) {
     a.threads = all * a.tiles;
     const long long blocks = (a.threads + 127) / 128;
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-    return launch(vec ? pick_conv<T, VEC>(a.k) : pick_conv<T, 1>(a.k), dim3((unsigned)blocks), 128, 0, st, a);
+    return launch(vec == VEC ? pick_conv<T, VEC>(a.k) : vec == 2 ? pick_conv<T, 2>(a.k) : pick_conv<T, 1>(a.k), dim3((unsigned)blocks), 128, 0, st, a);
 }
 
 }  // namespace seq

@@ -1,5 +1,7 @@
 // seq_scan.cu -- the selective scan: argument checks, the choice of kernel, and the kernel for
 // single tokens.  The kernel for prompts is in seq_scan.cuh.
+#include <math.h>
+
 #include "seq_scan.cuh"
 
 namespace fcm {
@@ -218,7 +220,7 @@ template <typename T> static ScanChoice choose_scan(const ScanArgs &a, int sms) 
         const double pair = 2 * scan_smem<T>(s.spt, s.lpc) <= 227 * 1024 ? 1.68 : 2.0;
         for (int parts = 1; parts <= 8; parts *= 2) {
             const double blocks = (double)a.q.n_seq * a.groups * ((a.cpg + ch - 1) / ch) * parts;
-            const double load = blocks * (filled < 1.0 ? filled : 1.0) / (2.0 * sms);
+            const double load = ceil(blocks * (filled < 1.0 ? filled : 1.0) / (2.0 * sms));
             const double step = blocks <= sms ? s.t1 : s.t1 * pair * (load > 1.0 ? load : 1.0);
             const double ns = parts == 1 ? step * rows : 1.69 * step * rows / parts + 4000.0;
             if (ns < least) least = ns, best = {s.spt, s.lpc, parts};
