@@ -64,9 +64,10 @@ template <typename T> __device__ __forceinline__ uint32_t two_weights(uint32_t q
 // long as both sides follow it: a 32-bit word of eight weights gives the pairs (0,4), (1,5),
 // (2,6), (3,7) with a shift and a mask each, and the inputs are paired alike.  So weights go
 // from memory to the tensor cores as whole numbers, without a detour, and a group's sum is
-// scaled in 32 bits.  XV: x's rows are 16-byte aligned.
-template <typename T, int G, int NT, bool XV>
-__global__ void __launch_bounds__(512, NT == 1 && G >= 64 ? 2 : 1) w4_kernel(const W4Args a) {
+// scaled in 32 bits.  XV: x's rows are 16-byte aligned.  SV: four scales are loaded at once, since a
+// load whose lanes read eight rows takes eight turns at the cache whatever it brings.
+template <typename T, int G, int NT, bool XV, bool SV>
+__global__ void __launch_bounds__(512, NT == 1 ? 2 : 1) w4_kernel(const W4Args a) {
     constexpr int WORDS = G / 32;   // words per lane and group
     constexpr int UB = 128 / G;     // groups loaded at once
     extern __shared__ float red[];
@@ -136,21 +137,32 @@ __global__ void __launch_bounds__(512, NT == 1 && G >= 64 ? 2 : 1) w4_kernel(con
                 sum[i][j] = fmaf(v, j < 2 ? fa : fb, sum[i][j]);
             }
     };
-    const int per = (a.units + warps * UB - 1) / (warps * UB) * UB, u0 = min(a.units, warp * per), u1 = min(a.units, u0 + per);
+    constexpr int STEP = SV ? 4 : UB;   // groups a warp's share is a multiple of
+    const int per = (a.units + warps * STEP - 1) / (warps * STEP) * STEP;
+    const int u0 = min(a.units, warp * per), u1 = min(a.units, u0 + per);
     const int whole = min(u1, a.in / G);   // the last group may be short
     int u = u0;
-    for (; u + UB <= whole; u += UB) {
-        Words qa[UB], qb[UB];
-        float fa[UB], fb[UB];
+    for (; u + STEP <= whole; u += STEP) {
+        Vec<T, STEP> fa, fb;
+        if (SV) {
+            fa = *reinterpret_cast<const Vec<T, STEP> *>(sa + u);
+            fb = *reinterpret_cast<const Vec<T, STEP> *>(sb + u);
+        } else {
 #pragma unroll
-        for (int i = 0; i < UB; i++) {
-            qa[i] = *reinterpret_cast<const Words *>(wa + (size_t)(u + i) * (G / 2));
-            qb[i] = *reinterpret_cast<const Words *>(wb + (size_t)(u + i) * (G / 2));
-            fa[i] = Storage<T>::to_f(sa[u + i]);
-            fb[i] = Storage<T>::to_f(sb[u + i]);
+            for (int i = 0; i < STEP; i++) fa.e[i] = sa[u + i], fb.e[i] = sb[u + i];
         }
 #pragma unroll
-        for (int i = 0; i < UB; i++) group(inputs(u + i), qa[i], qb[i], fa[i], fb[i]);
+        for (int v = 0; v < STEP; v += UB) {
+            Words qa[UB], qb[UB];
+#pragma unroll
+            for (int i = 0; i < UB; i++) {
+                qa[i] = *reinterpret_cast<const Words *>(wa + (size_t)(u + v + i) * (G / 2));
+                qb[i] = *reinterpret_cast<const Words *>(wb + (size_t)(u + v + i) * (G / 2));
+            }
+#pragma unroll
+            for (int i = 0; i < UB; i++)
+                group(inputs(u + v + i), qa[i], qb[i], Storage<T>::to_f(fa.e[v + i]), Storage<T>::to_f(fb.e[v + i]));
+        }
     }
     for (; u < u1; u++) {
         const bool in = u * G + t * (G / 4) < a.in;   // a short group ends with a lane's quarter
@@ -183,11 +195,19 @@ __global__ void __launch_bounds__(512, NT == 1 && G >= 64 ? 2 : 1) w4_kernel(con
 template <typename T, int G>
 static cudaError_t run_w4(const W4Args &a, int sms, cudaStream_t st) {
     const unsigned tiles = (unsigned)((a.out + 15) / 16), gy = (unsigned)((a.m + 15) / 16);
-    int warps = tiles * gy >= 2u * sms ? 8 : 16;
+    // More warps share the inputs where the tiles leave SMs without a block, fewer where most SMs hold
+    // two blocks and some a third.  Measured, us with 16, 8 and 4 warps: 4096 x 4096 (256 tiles) 4.3,
+    // 5.4, -; 5003 x 4096 in groups of 32, 7 tokens (313) 8.4, 9.3, 7.5; 16384 x 8192 in groups
+    // of 64 (1024) 25.2, 23.1, 26.8; 5120 x 5120, 16 tokens (320) 14.6, 12.1, 11.9.
+    const unsigned long long blocks = (unsigned long long)tiles * gy;
+    int warps = blocks < 2ull * sms ? 16 : blocks < 3ull * sms ? 4 : 8;
     while (warps > 4 && warps / 2 >= a.units) warps /= 2;
     const bool xv = aligned16(a.x) && a.ld_x % 8 == 0, wide = a.m > 8;
-    void (*kernel)(W4Args) = wide ? (xv ? w4_kernel<T, G, 2, true> : w4_kernel<T, G, 2, false>)
-                                  : (xv ? w4_kernel<T, G, 1, true> : w4_kernel<T, G, 1, false>);
+    // where that leaves no warp without work
+    const bool sv = xv && !wide && a.units % 4 == 0 && a.units >= 4 * warps && reinterpret_cast<uintptr_t>(a.qs) % 8 == 0;
+    void (*kernel)(W4Args) =
+        wide ? (xv ? w4_kernel<T, G, 2, true, false> : w4_kernel<T, G, 2, false, false>)
+             : (sv ? w4_kernel<T, G, 1, true, true> : xv ? w4_kernel<T, G, 1, true, false> : w4_kernel<T, G, 1, false, false>);
     return launch(kernel, dim3(tiles, gy), warps * 32, (size_t)warps * (wide ? 256 : 128) * 4, st, a);
 }
 
