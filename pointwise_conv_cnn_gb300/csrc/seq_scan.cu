@@ -310,8 +310,10 @@ extern "C" fcm_status fcm_selective_scan(const fcm_scan_desc *desc, const void *
     k.cpg = d.c / d.groups;
     const size_t e16 = 16 / e;
     const long long starts = d.groups == 1 ? 0 : k.cpg | d.n_state;   // a group's first column
-    k.vec16 = seq::aligned16(x) && seq::aligned16(dt) && seq::aligned16(bm) && seq::aligned16(cm) &&
-              seq::aligned16(z) && ((d.ld_x | d.ld_dt | d.ld_b | d.ld_c | (z ? d.ld_z : 0) | starts) % e16) == 0;
+    k.vec16 = seq::aligned16(x) && seq::aligned16(dt) && seq::aligned16(z) &&
+              ((d.ld_x | d.ld_dt | (z ? d.ld_z : 0) | (d.groups == 1 ? 0 : k.cpg)) % e16) == 0;
+    k.vec16n = seq::aligned16(bm) && seq::aligned16(cm) &&
+               ((d.ld_b | d.ld_c | (d.groups == 1 ? 0 : d.n_state)) % e16) == 0;
     k.vec2 = reinterpret_cast<uintptr_t>(y) % (2 * e) == 0 && (d.ld_y | starts) % 2 == 0;
     const cudaError_t ce = d.dtype == FCM_F32   ? seq::run_scan<float>(k, sms, static_cast<cudaStream_t>(stream))
                            : d.dtype == FCM_F16 ? seq::run_scan<__half>(k, sms, static_cast<cudaStream_t>(stream))

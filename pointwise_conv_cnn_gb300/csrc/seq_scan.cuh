@@ -21,7 +21,8 @@ struct ScanArgs {
     int c, n, groups, softplus;
     int cpg;        // channels per group
     int blocks;     // channel blocks per group
-    int vec16;      // every block's row of x, dt, z, bm, cm starts on 16 bytes
+    int vec16;      // every block's row of x, dt and z starts on 16 bytes
+    int vec16n;     // every row of bm and cm starts on 16 bytes
     int vec2;       // every block's row of y starts on two elements
 };
 
@@ -90,9 +91,6 @@ __device__ __forceinline__ float ld_cluster(uint32_t local, int rank) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -100,20 +98,10 @@ template <int N> __device__ __forceinline__ void cp_wait() {
 
 // A tile's rows lie 16 bytes further apart than their length, which keeps lanes that read different
 // rows on different banks.  16-byte aligned rows are copied in 16-byte pieces; others in the
-// aligned 4-byte words that hold their bytes, each row at the offset that its address has within
-// a word.  What lies past a tile's rows or a row's elements is left as it was and not used.
+// aligned pieces that hold their bytes, each row at the offset that its address has within a
+// piece (an allocation starts on a piece, and of the last piece no more than the row is read).
+// What lies past a tile's rows or a row's elements is not used.
 constexpr int row_pitch(int rb) { return (rb < 16 ? 16 : rb) + 16; }
-
-template <int ROWS, int RB>
-__device__ __forceinline__ void copy_words(uint32_t dst, const char *src, long long stride, int rows, int valid, int tid) {
-    constexpr int NP = RB / 4 + 1;
-    for (int i = tid; i < ROWS * NP; i += 128) {
-        const int r = i / NP, p = i % NP;
-        const char *row = src + r * stride;
-        const int rest = (int)(reinterpret_cast<uintptr_t>(row) & 3);
-        if (r < rows && p * 4 < valid + rest) cp_async4(dst + r * row_pitch(RB) + p * 4, row - rest + p * 4);
-    }
-}
 // A barrier of the four warps that do not scan.
 __device__ __forceinline__ void helpers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -154,7 +142,8 @@ template <typename T> __device__ __forceinline__ void store_pair(T *p, float a, 
 }
 
 // ------------------------------------------------------------------ the kernel
-// SPT states per thread, LPC lanes per channel (SPT * LPC >= n; FULL: equal).  Four warps scan:
+// SPT states per thread, LPC lanes per channel (SPT * LPC >= n).  PAD: 0, n is their product; 1, a
+// lane's states all exist or none does; 2, neither.  Four warps scan:
 // a warp holds 32 / LPC channels, lane = part * channels + channel, so that the lanes that read
 // one part of B and C are neighbours and the read is a broadcast.  Four more warps do what is
 // per channel and token: they load, make the steps D and D * x and widen B and C for the tile
@@ -178,7 +167,7 @@ template <typename T, int SPT, int LPC> struct ScanShape {
     static constexpr int SMEM = NST * STAGE + 2 * (DU + BC + OUT);   // and JOIN where sequences are split
 };
 
-template <typename T, int SPT, int LPC, bool FULL, bool SPLIT>
+template <typename T, int SPT, int LPC, int PAD, bool SPLIT>
 __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
     typedef ScanShape<T, SPT, LPC> S;
     constexpr int TT = S::TT, CH = S::CH, CHW = S::CHW, NP = S::NP;
@@ -220,7 +209,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
             float v[SPT];
 #pragma unroll
             for (int i = 0; i < SPT; i++) {
-                const bool in = live && (FULL || n0 + i < a.n);
+                const bool in = live && (PAD == 0 || n0 + i < a.n);
                 v[i] = in ? a.a[at + i] * kLog2e : 0.0f;
                 h0[i] = in && row >= 0 && a.state_in ? a.state_in[(size_t)row * a.c * a.n + at + i] : 0.0f;
             }
@@ -252,7 +241,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                         if (OUT) {
                             const ulonglong2 c2 = *reinterpret_cast<const ulonglong2 *>(bc + r * 2 * NP + NP + 2 * j);
                             f32x2 s0 = h[j], s1 = h[j + 1];
-                            if (!FULL) {   // a padding state's 0 * infinity stays out of the sum
+                            if (PAD == 2) {   // a padding state's 0 * infinity stays out of the sum
                                 float p0, p1, p2, p3;
                                 unpack2(s0, p0, p1);
                                 unpack2(s1, p2, p3);
@@ -266,7 +255,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                     }
                     float lo, hi;
                     unpack2(add2(acc0, acc1), lo, hi);
-                    return lo + hi;
+                    return PAD == 1 && n0 >= a.n ? 0.0f : lo + hi;
                 };
                 const int rows = min(TT, t1 - t0 - k * TT);
                 if (rows == TT) {
@@ -325,14 +314,14 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
             for (int i = 0; i < SPT; i++) {
                 float lo, hi;
                 unpack2(h[i / 2], lo, hi);
-                if (FULL || n0 + i < a.n) to[i] = i & 1 ? hi : lo;
+                if (PAD == 0 || n0 + i < a.n) to[i] = i & 1 ? hi : lo;
             }
         }
     } else {
         // ---------------------------------------------------------------- the others
         const int tid = threadIdx.x - S::NS;
-        auto help = [&](auto vec_tag) {
-            constexpr bool vec16 = decltype(vec_tag)::value;
+        auto help = [&](auto vec_tag, auto vecn_tag) {
+            constexpr bool vec16 = decltype(vec_tag)::value, vec16n = decltype(vecn_tag)::value;
             constexpr int E = (int)sizeof(T), NST = S::NST, PITCHX = row_pitch(S::RBX), PITCHN = row_pitch(S::RBN);
             const uint32_t sm = tc::smem_u32(smem);
             const long long bx = a.ld_x * E, bdt = a.ld_dt * E, bz = a.ld_z * E, bb = a.ld_b * E, bc = a.ld_c * E;
@@ -344,7 +333,8 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
             const char *pc = static_cast<const char *>(a.cm) + first * bc + (long long)g * a.n * E;
 
             // ---- copies: a tile's rows, asynchronously, two tiles ahead of their use
-            constexpr int NPX = S::RBX < 16 ? 1 : S::RBX / 16, NPN = S::RBN < 16 ? 1 : S::RBN / 16;   // pieces of a row
+            constexpr int NPX = (S::RBX < 16 ? 1 : S::RBX / 16) + !vec16;   // pieces of a row
+            constexpr int NPN = (S::RBN < 16 ? 1 : S::RBN / 16) + !vec16n;
             constexpr int RX = 128 / NPX < TT ? 128 / NPX : TT, RN = 128 / NPN < TT ? 128 / NPN : TT; // rows at once
             const int rx = tid / NPX, qx = tid % NPX * 16, rn = tid / NPN, qn = tid % NPN * 16;
             const int nx = rx < TT ? max(0, min(16, valid * E - qx)) : 0, nn = rn < TT ? max(0, min(16, a.n * E - qn)) : 0;
@@ -354,6 +344,16 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
 #pragma unroll
                     for (int i = 0; i < TT; i += R)
                         if (r + i < rows) cp_async16(to + i * PITCH, from + i * stride, n);
+                }
+            };
+            auto copy_any = [&](auto rows_tag, auto pitch_tag, uint32_t to, const char *from, long long stride, int r, int q, int n, int rows) {
+                constexpr int R = decltype(rows_tag)::value, PITCH = decltype(pitch_tag)::value;
+                if (r >= R) return;   // the last threads, where the pieces do not divide them
+#pragma unroll
+                for (int i = 0; i < TT; i += R) {
+                    const char *p = from + i * stride;
+                    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15), m = min(16, n + off - q);
+                    if ((TT % R == 0 || r + i < TT) && r + i < rows && m > 0) cp_async16(to + i * PITCH, p - off, m);
                 }
             };
             typedef std::integral_constant<int, RX> RowsX;
@@ -366,26 +366,23 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                 if (k < tiles) {
                     const uint32_t at = sm + (k % NST) * S::STAGE;
                     const int rows = t1 - t0 - k * TT;
-                    if constexpr (vec16) {
-                        const uint32_t ax = at + rx * PITCHX + qx, an = at + 3 * S::X_BYTES + rn * PITCHN + qn;
-                        copy(RowsX{}, PitchX{}, ax, sx, bx, rx, nx, rows);
-                        copy(RowsX{}, PitchX{}, ax + S::X_BYTES, sdt, bdt, rx, nx, rows);
-                        copy(RowsN{}, PitchN{}, an, sb, bb, rn, nn, rows);
-                        if (with_out) {
-                            if (a.z) copy(RowsX{}, PitchX{}, ax + 2 * S::X_BYTES, sz, bz, rx, nx, rows);
-                            copy(RowsN{}, PitchN{}, an + S::N_BYTES, sc, bc, rn, nn, rows);
-                        }
-                        sx += TT * bx, sdt += TT * bdt, sz += TT * bz, sb += TT * bb, sc += TT * bc;
-                    } else {
-                        const long long t = (long long)k * TT;
-                        copy_words<TT, S::RBX>(at, px + t * bx, bx, rows, valid * E, tid);
-                        copy_words<TT, S::RBX>(at + S::X_BYTES, pdt + t * bdt, bdt, rows, valid * E, tid);
-                        copy_words<TT, S::RBN>(at + 3 * S::X_BYTES, pb + t * bb, bb, rows, a.n * E, tid);
-                        if (with_out) {
-                            if (a.z) copy_words<TT, S::RBX>(at + 2 * S::X_BYTES, pz + t * bz, bz, rows, valid * E, tid);
-                            copy_words<TT, S::RBN>(at + 3 * S::X_BYTES + S::N_BYTES, pc + t * bc, bc, rows, a.n * E, tid);
-                        }
+                    const uint32_t ax = at + rx * PITCHX + qx, an = at + 3 * S::X_BYTES + rn * PITCHN + qn;
+                    auto copy_x = [&](uint32_t to, const char *from, long long stride) {
+                        if constexpr (vec16) copy(RowsX{}, PitchX{}, to, from, stride, rx, nx, rows);
+                        else copy_any(RowsX{}, PitchX{}, to, from, stride, rx, qx, valid * E, rows);
+                    };
+                    auto copy_n = [&](uint32_t to, const char *from, long long stride) {
+                        if constexpr (vec16n) copy(RowsN{}, PitchN{}, to, from, stride, rn, nn, rows);
+                        else copy_any(RowsN{}, PitchN{}, to, from, stride, rn, qn, a.n * E, rows);
+                    };
+                    copy_x(ax, sx, bx);
+                    copy_x(ax + S::X_BYTES, sdt, bdt);
+                    copy_n(an, sb, bb);
+                    if (with_out) {
+                        if (a.z) copy_x(ax + 2 * S::X_BYTES, sz, bz);
+                        copy_n(an + S::N_BYTES, sc, bc);
                     }
+                    sx += TT * bx, sdt += TT * bdt, sz += TT * bz, sb += TT * bb, sc += TT * bc;
                 }
                 cp_commit();
             };
@@ -403,9 +400,9 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                     if (a.skip) skip[i] = a.skip[c0 + ch + i];
                 }
             T *py = static_cast<T *>(a.y) + (first + r0) * a.ld_y + c0 + ch;
-            // where row r of a tile starts within its place: copies of words keep the address's rest
+            // where row r of a tile starts within its place: the copies keep the address's rest
             auto rest = [&](const char *p, long long stride, int r) {
-                return vec16 ? 0u : (uint32_t)((reinterpret_cast<uintptr_t>(p) + (uintptr_t)(r * stride)) & 3);
+                return ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)r * (uint32_t)stride) & 15;
             };
             auto prepare = [&](int k, bool with_c) {
                 const unsigned char *raw = smem + (k % NST) * S::STAGE;
@@ -448,11 +445,11 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                         for (int i = 0; i < QT; i++) {
                             const int r = rq + i * QS;
                             const unsigned char *p = from + r * PITCHN;
-                            if (!vec16) p += which ? rest(pc, bc, k * TT + r) : rest(pb, bb, k * TT + r);
                             float4 v;
-                            get_pair<T>(p, vec16, v.x, v.y);
-                            get_pair<T>(p + 2 * E, vec16, v.z, v.w);
-                            if (!FULL) {   // padding states: nothing in, nothing out
+                            if (!vec16n) p += which ? rest(pc, bc, k * TT + r) : rest(pb, bb, k * TT + r);
+                            get_pair<T>(p, vec16n, v.x, v.y);
+                            get_pair<T>(p + 2 * E, vec16n, v.z, v.w);
+                            if (PAD) {   // padding states: nothing in, nothing out
                                 v.x = n4 < a.n ? v.x : 0.0f, v.y = n4 + 1 < a.n ? v.y : 0.0f;
                                 v.z = n4 + 2 < a.n ? v.z : 0.0f, v.w = n4 + 3 < a.n ? v.w : 0.0f;
                             }
@@ -493,7 +490,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                     for (int i = 0; i < IT; i++) {
                         const int r = r0 + i * RS;
                         float x, y;
-                        get_pair<T>(raw + r * PITCHX + ch * E + rest(px, bx, k * TT + r), vec16, x, y);
+                        get_pair<T>(raw + r * PITCHX + ch * E + (vec16 ? 0 : rest(px, bx, k * TT + r)), vec16, x, y);
                         o[i][0] = fmaf(skip[0], x, o[i][0]);
                         o[i][1] = fmaf(skip[1], y, o[i][1]);
                     }
@@ -502,7 +499,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                     for (int i = 0; i < IT; i++) {
                         const int r = r0 + i * RS;
                         float x, y;
-                        get_pair<T>(raw + 2 * S::X_BYTES + r * PITCHX + ch * E + rest(pz, bz, k * TT + r), vec16, x, y);
+                        get_pair<T>(raw + 2 * S::X_BYTES + r * PITCHX + ch * E + (vec16 ? 0 : rest(pz, bz, k * TT + r)), vec16, x, y);
                         o[i][0] *= silu(x);
                         o[i][1] *= silu(y);
                     }
@@ -537,8 +534,9 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
             }
             serve(true);
         };
-        if (a.vec16) help(std::true_type{});
-        else help(std::false_type{});
+        if (a.vec16 && a.vec16n) help(std::true_type{}, std::true_type{});
+        else if (a.vec16) help(std::true_type{}, std::false_type{});
+        else help(std::false_type{}, std::false_type{});
     }
     if constexpr (SPLIT) cluster_sync();   // the others may still be reading this block's part
 }
@@ -550,7 +548,7 @@ template <typename T> constexpr int scan_smem(int spt, int lpc) {
 }
 
 // Launches the kernel of one shape; `parts` blocks of a cluster share a sequence.
-template <typename T, int SPT, int LPC, bool FULL>
+template <typename T, int SPT, int LPC, int PAD>
 cudaError_t launch_scan_shape(ScanArgs a, int parts, cudaStream_t st) {
     typedef ScanShape<T, SPT, LPC> S;
     static_assert(S::SMEM == scan_smem<T>(SPT, LPC), "");
@@ -559,8 +557,8 @@ cudaError_t launch_scan_shape(ScanArgs a, int parts, cudaStream_t st) {
     const long long grid = (long long)a.q.n_seq * a.groups * a.blocks * parts;
     if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
     const int smem = S::SMEM + (parts > 1 ? S::JOIN : 0);
-    void (*kernel)(ScanArgs) = parts > 1 ? scan_kernel<T, SPT, LPC, FULL, true>
-                                         : scan_kernel<T, SPT, LPC, FULL, false>;
+    void (*kernel)(ScanArgs) = parts > 1 ? scan_kernel<T, SPT, LPC, PAD, true>
+                                         : scan_kernel<T, SPT, LPC, PAD, false>;
     if (smem > 48 * 1024) {   // raised once per context, as for the tensor-core kernels
         std::atomic<unsigned long long> &known = attr_ctx[parts > 1];
         const unsigned long long ctx = fcm_current_ctx_id();
@@ -580,18 +578,20 @@ template <typename T> cudaError_t launch_scan(const ScanArgs &a, int spt, int lp
 #define FCM_SCAN_INSTANTIATE(T)                                                                      \
     template <>                                                                                      \
     cudaError_t launch_scan<T>(const ScanArgs &a, int spt, int lpc, int parts, cudaStream_t st) {    \
-        const bool full = a.n == spt * lpc;                                                          \
-        switch (spt * 256 + lpc * 2 + full) {                                                        \
+        const int pad = a.n == spt * lpc ? 0 : a.n % spt == 0 ? 1 : 2;                               \
+        switch (spt * 256 + lpc * 4 + pad) {                                                         \
             FCM_SCAN_CASE(T, 4, 1, 0) FCM_SCAN_CASE(T, 4, 2, 0) FCM_SCAN_CASE(T, 4, 4, 0)            \
             FCM_SCAN_CASE(T, 4, 8, 0) FCM_SCAN_CASE(T, 8, 8, 0) FCM_SCAN_CASE(T, 8, 16, 0)           \
-            FCM_SCAN_CASE(T, 4, 1, 1) FCM_SCAN_CASE(T, 4, 2, 1) FCM_SCAN_CASE(T, 4, 4, 1)            \
-            FCM_SCAN_CASE(T, 4, 8, 1) FCM_SCAN_CASE(T, 8, 8, 1) FCM_SCAN_CASE(T, 8, 16, 1)           \
-            FCM_SCAN_CASE(T, 8, 2, 1) FCM_SCAN_CASE(T, 8, 4, 1) FCM_SCAN_CASE(T, 16, 1, 1)           \
+            FCM_SCAN_CASE(T, 8, 2, 0) FCM_SCAN_CASE(T, 8, 4, 0) FCM_SCAN_CASE(T, 16, 1, 0)           \
+            FCM_SCAN_CASE(T, 4, 4, 1) FCM_SCAN_CASE(T, 4, 8, 1) FCM_SCAN_CASE(T, 8, 8, 1)            \
+            FCM_SCAN_CASE(T, 8, 16, 1)                                                               \
+            FCM_SCAN_CASE(T, 4, 1, 2) FCM_SCAN_CASE(T, 4, 2, 2) FCM_SCAN_CASE(T, 4, 4, 2)            \
+            FCM_SCAN_CASE(T, 4, 8, 2) FCM_SCAN_CASE(T, 8, 8, 2) FCM_SCAN_CASE(T, 8, 16, 2)           \
         }                                                                                            \
         return cudaErrorInvalidValue;                                                                \
     }
-#define FCM_SCAN_CASE(T, SPT, LPC, FULL) \
-    case SPT * 256 + LPC * 2 + FULL: return launch_scan_shape<T, SPT, LPC, FULL>(a, parts, st);
+#define FCM_SCAN_CASE(T, SPT, LPC, PAD) \
+    case SPT * 256 + LPC * 4 + PAD: return launch_scan_shape<T, SPT, LPC, PAD>(a, parts, st);
 
 }  // namespace seq
 }  // namespace fcm
