@@ -58,28 +58,33 @@ template <typename T> __device__ __forceinline__ uint32_t two_weights(uint32_t q
     return r;
 }
 
-// One block: 16 outputs of up to 8 * NT tokens; its warps share the inputs' groups.  A lane of row
-// r = lane / 4 and quarter t = lane % 4 holds the weights of rows r and r + 8 in quarter t of a
+// One block: 16 * MT outputs of up to 8 * NT tokens; its warps share the inputs' groups.  A lane of row
+// r = lane / 4 and quarter t = lane % 4 holds the weights of rows r, r + 8, .. in quarter t of a
 // group, and the inputs of token r there.  The product's inner index may run in any order as
 // long as both sides follow it: a 32-bit word of eight weights gives the pairs (0,4), (1,5),
 // (2,6), (3,7) with a shift and a mask each, and the inputs are paired alike.  So weights go
 // from memory to the tensor cores as whole numbers, without a detour, and a group's sum is
 // scaled in 32 bits.  XV: x's rows are 16-byte aligned.  SV: four scales are loaded at once, since a
 // load whose lanes read eight rows takes eight turns at the cache whatever it brings.
-template <typename T, int G, int NT, bool XV, bool SV>
-__global__ void __launch_bounds__(512, NT == 1 ? 2 : 1) w4_kernel(const W4Args a) {
+template <typename T, int G, int MT, int NT, bool XV, bool SV>
+__global__ void __launch_bounds__(512, MT * NT == 1 ? 2 : 1) w4_kernel(const W4Args a) {
     constexpr int WORDS = G / 32;   // words per lane and group
     constexpr int UB = 128 / G;     // groups loaded at once
+    constexpr int R = 2 * MT, OB = 16 * MT;   // rows of a lane, outputs of a block
     extern __shared__ float red[];
     tc::pdl_wait();
     tc::pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int r = lane >> 2, t = lane & 3, o0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
-    // rows past the last output repeat it
-    const int oa = min(o0 + r, a.out - 1), ob = min(o0 + r + 8, a.out - 1);
-    const uint8_t *wa = static_cast<const uint8_t *>(a.qw) + (size_t)oa * (a.in / 2) + t * (G / 8);
-    const uint8_t *wb = static_cast<const uint8_t *>(a.qw) + (size_t)ob * (a.in / 2) + t * (G / 8);
-    const T *sa = static_cast<const T *>(a.qs) + (size_t)oa * a.units, *sb = static_cast<const T *>(a.qs) + (size_t)ob * a.units;
+    const int r = lane >> 2, t = lane & 3, m0 = blockIdx.y * 16;
+    const unsigned o0 = blockIdx.x * OB;
+    const uint8_t *wr[R];
+    const T *sr[R];
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+        const unsigned o = min(o0 + r + 8 * i, (unsigned)a.out - 1);   // rows past the last output repeat it
+        wr[i] = static_cast<const uint8_t *>(a.qw) + (size_t)o * (a.in / 2) + t * (G / 8);
+        sr[i] = static_cast<const T *>(a.qs) + (size_t)o * a.units;
+    }
     // A column of the product is a token's alone.  Where there are fewer tokens, its inputs are not
     // read (the lanes of one token alone take a quarter of the cache's bandwidth that all take).
     const T *x[NT];
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(512, NT == 1 ? 2 : 1) w4_kernel(const W4Args a
         token[i] = m0 + i * 8 + r < a.m;
         x[i] = static_cast<const T *>(a.x) + (long long)min(m0 + i * 8 + r, a.m - 1) * a.ld_x + t * (G / 4);
     }
-    float sum[NT][4] = {};
+    float sum[MT][NT][4] = {};
     struct alignas(4 * WORDS) Words {
         uint32_t w[WORDS];
     };
@@ -113,29 +118,47 @@ __global__ void __launch_bounds__(512, NT == 1 ? 2 : 1) w4_kernel(const W4Args a
             }
         return in;
     };
-    auto group = [&](const Inputs &in, const Words &qa, const Words &qb, float fa, float fb) {
-        constexpr int SUMS = WORDS >= 4 ? 2 : 1;   // a long group's products need not wait for each other
-        float c[SUMS][NT][4] = {};
+    struct Weights {
+        Words q[R];
+    };
+    auto weights = [&](int u) {
+        Weights v;
+#pragma unroll
+        for (int i = 0; i < R; i++) v.q[i] = *reinterpret_cast<const Words *>(wr[i] + (size_t)u * (G / 2));
+        return v;
+    };
+    auto group = [&](const Inputs &in, const Weights &q, const float (&f)[R]) {
+        constexpr int SUMS = WORDS >= 4 && MT == 1 ? 2 : 1;   // a long group's products need not wait for each other
+        float c[SUMS][MT][NT][4] = {};
 #pragma unroll
         for (int w = 0; w < WORDS; w++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                const uint32_t f[4] = {two_weights<T>(qa.w[w], 2 * h), two_weights<T>(qb.w[w], 2 * h),
-                                       two_weights<T>(qa.w[w], 2 * h + 1), two_weights<T>(qb.w[w], 2 * h + 1)};
+                uint32_t b[NT][2];
 #pragma unroll
                 for (int i = 0; i < NT; i++) {
                     const uint4 v = in.v[i][w];
                     const uint32_t lo = h ? v.y : v.x, hi = h ? v.w : v.z;
-                    mma16816<T>(c[h % SUMS][i], f, __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+                    b[i][0] = __byte_perm(lo, hi, 0x5410), b[i][1] = __byte_perm(lo, hi, 0x7632);
+                }
+#pragma unroll
+                for (int k = 0; k < MT; k++) {
+                    const uint32_t qa = q.q[2 * k].w[w], qb = q.q[2 * k + 1].w[w];
+                    const uint32_t m[4] = {two_weights<T>(qa, 2 * h), two_weights<T>(qb, 2 * h),
+                                           two_weights<T>(qa, 2 * h + 1), two_weights<T>(qb, 2 * h + 1)};
+#pragma unroll
+                    for (int i = 0; i < NT; i++) mma16816<T>(c[h % SUMS][k][i], m, b[i][0], b[i][1]);
                 }
             }
 #pragma unroll
-        for (int i = 0; i < NT; i++)
+        for (int k = 0; k < MT; k++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float v = SUMS == 2 ? c[0][i][j] + c[SUMS - 1][i][j] : c[0][i][j];
-                sum[i][j] = fmaf(v, j < 2 ? fa : fb, sum[i][j]);
-            }
+            for (int i = 0; i < NT; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float v = SUMS == 2 ? c[0][k][i][j] + c[SUMS - 1][k][i][j] : c[0][k][i][j];
+                    sum[k][i][j] = fmaf(v, f[2 * k + j / 2], sum[k][i][j]);
+                }
     };
     constexpr int STEP = SV ? 4 : UB;   // groups a warp's share is a multiple of
     const int per = (a.units + warps * STEP - 1) / (warps * STEP) * STEP;
@@ -143,71 +166,110 @@ __global__ void __launch_bounds__(512, NT == 1 ? 2 : 1) w4_kernel(const W4Args a
     const int whole = min(u1, a.in / G);   // the last group may be short
     int u = u0;
     for (; u + STEP <= whole; u += STEP) {
-        Vec<T, STEP> fa, fb;
-        if (SV) {
-            fa = *reinterpret_cast<const Vec<T, STEP> *>(sa + u);
-            fb = *reinterpret_cast<const Vec<T, STEP> *>(sb + u);
-        } else {
+        Vec<T, STEP> f[R];
 #pragma unroll
-            for (int i = 0; i < STEP; i++) fa.e[i] = sa[u + i], fb.e[i] = sb[u + i];
+        for (int j = 0; j < R; j++) {
+            if (SV) {
+                f[j] = *reinterpret_cast<const Vec<T, STEP> *>(sr[j] + u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < STEP; i++) f[j].e[i] = sr[j][u + i];
+            }
         }
 #pragma unroll
         for (int v = 0; v < STEP; v += UB) {
-            Words qa[UB], qb[UB];
+            Weights q[UB];
+#pragma unroll
+            for (int i = 0; i < UB; i++) q[i] = weights(u + v + i);
 #pragma unroll
             for (int i = 0; i < UB; i++) {
-                qa[i] = *reinterpret_cast<const Words *>(wa + (size_t)(u + v + i) * (G / 2));
-                qb[i] = *reinterpret_cast<const Words *>(wb + (size_t)(u + v + i) * (G / 2));
-            }
+                float g[R];
 #pragma unroll
-            for (int i = 0; i < UB; i++)
-                group(inputs(u + v + i), qa[i], qb[i], Storage<T>::to_f(fa.e[v + i]), Storage<T>::to_f(fb.e[v + i]));
+                for (int j = 0; j < R; j++) g[j] = Storage<T>::to_f(f[j].e[v + i]);
+                group(inputs(u + v + i), q[i], g);
+            }
         }
     }
     for (; u < u1; u++) {
         const bool in = u * G + t * (G / 4) < a.in;   // a short group ends with a lane's quarter
-        Words qa = {}, qb = {};
+        Weights q = {};
         Inputs v = {};                                // whose inputs past the end are zeros
         if (in) {
-            qa = *reinterpret_cast<const Words *>(wa + (size_t)u * (G / 2));
-            qb = *reinterpret_cast<const Words *>(wb + (size_t)u * (G / 2));
+            q = weights(u);
             v = inputs(u);
         }
-        group(v, qa, qb, Storage<T>::to_f(sa[u]), Storage<T>::to_f(sb[u]));
+        float g[R];
+#pragma unroll
+        for (int j = 0; j < R; j++) g[j] = Storage<T>::to_f(sr[j][u]);
+        group(v, q, g);
     }
     // the warps' sums, in their order
+    constexpr int SUM = NT * 8 * OB;
 #pragma unroll
-    for (int i = 0; i < NT; i++)
+    for (int k = 0; k < MT; k++)
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            red[(warp * NT * 8 + i * 8 + 2 * t + (j & 1)) * 16 + r + (j >> 1) * 8] = sum[i][j];
+        for (int i = 0; i < NT; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                red[warp * SUM + (i * 8 + 2 * t + (j & 1)) * OB + k * 16 + r + (j >> 1) * 8] = sum[k][i][j];
     __syncthreads();
-    for (int i = threadIdx.x; i < NT * 128; i += blockDim.x) {
-        const int tok = m0 + i / 16, o = o0 + i % 16;
-        if (tok >= a.m || o >= a.out) continue;
+    for (int i = threadIdx.x; i < SUM; i += blockDim.x) {
+        const int tok = m0 + i / OB;
+        const unsigned o = o0 + i % OB;
+        if (tok >= a.m || o >= (unsigned)a.out) continue;
         float v = 0.0f;
-        for (int w = 0; w < warps; w++) v += red[w * NT * 128 + i];
+        for (int w = 0; w < warps; w++) v += red[w * SUM + i];
         static_cast<T *>(a.y)[(long long)tok * a.ld_y + o] = Storage<T>::from_f(
             act_seq(fmaf(a.s ? a.s[o] : 1.0f, v, a.b ? a.b[o] : 0.0f), a.act));
     }
 }
 
+// One tile of 16 outputs a block or two.  Two halve the reads of the inputs, which with eight and
+// more tokens cost more than the weights' (a warp's 16 rows of weights in a group of 128 are 16 turns
+// at the cache, eight tokens' inputs 64), and their blocks need fewer rounds; one gives more
+// blocks and shorter ones.  Measured, us with one and two: 20480 x 8192 in groups of 128, 1, 8, 16 tokens
+// 28.0, 34.2, 61.6 and 27.5, 28.6, 42.0; 8192 x 8192 13.1, 15.0, 25.0 and 11.0, 12.0, 16.5; 16384 x
+// 4096 in groups of 64, 1, 8, 16 tokens 11.9, 12.4, 22.4 and 13.0, 13.9, 17.3.  One tile: groups of 32 (5003 x
+// 4096, 16 tokens 12.4 and 13.9), fewer blocks than half the SMs (2048 x 4096 5.2 and 6.7), short sums
+// (5120 x 1024 3.7 and 4.3), and up to 8 tokens scales that are not loaded by four (5120 x 5120, 1 token
+// 7.1 and 7.7).
+//
+// More warps share the inputs where the tiles leave SMs without a block, fewer where most SMs hold
+// two blocks and some a third.  Measured, us with 16, 8 and 4 warps, one tile: 3600 x 4096 in groups of 64 (225
+// blocks), 8 tokens 5.0, 4.8, 5.6; 2048 x 4096 (128) 3.2, 3.5, 4.8; 5003 x 4096 in groups of 32 (313) 7.5,
+// 7.9, 6.5; 16384 x 4096 in groups of 64 (1024) 12.9, 12.0, 13.6; two tiles, 16 tokens: 4096 x 4096 (128) 6.9, 7.2, 7.8;
+// 8192 x 8192 (256) 18.5, 17.2, 18.1.
 template <typename T, int G>
 static cudaError_t run_w4(const W4Args &a, int sms, cudaStream_t st) {
-    const unsigned tiles = (unsigned)((a.out + 15) / 16), gy = (unsigned)((a.m + 15) / 16);
-    // More warps share the inputs where the tiles leave SMs without a block, fewer where most SMs hold
-    // two blocks and some a third.  Measured, us with 16, 8 and 4 warps: 4096 x 4096 (256 tiles) 4.3,
-    // 5.4, -; 5003 x 4096 in groups of 32, 7 tokens (313) 8.4, 9.3, 7.5; 16384 x 8192 in groups
-    // of 64 (1024) 25.2, 23.1, 26.8; 5120 x 5120, 16 tokens (320) 14.6, 12.1, 11.9.
+    const bool xv = aligned16(a.x) && a.ld_x % 8 == 0, wide = a.m > 8;
+    // Scales by four, where that leaves the warps' shares nearly alike: 5120 x 5120 in groups of 128, 40 of
+    // them, 4 warps: 8.3 us by four, 7.1 one by one; 5003 x 4096 in groups of 32, 128 of them: 6.5, 8.5.
+    auto by_four = [&](int warps) {
+        const long long per = (a.units + 4 * warps - 1) / (4 * warps) * 4;
+        return xv && a.units % 4 == 0 && reinterpret_cast<uintptr_t>(a.qs) % 8 == 0 && per * warps * 8 <= a.units * 9ll;
+    };
+    const unsigned gy = (unsigned)((a.m + 15) / 16), pairs = ((unsigned)a.out + 31) / 32;
+    const unsigned long long blocks2 = (unsigned long long)pairs * gy;
+    if (xv && a.units >= 32 && 2 * blocks2 >= (unsigned long long)sms) {
+        if constexpr (G >= 64)
+            if (wide) {
+                const int warps = blocks2 <= (unsigned long long)sms ? 16 : 8;
+                return launch(by_four(warps) ? w4_kernel<T, G, 2, 2, true, true> : w4_kernel<T, G, 2, 2, true, false>,
+                              dim3(pairs, gy), warps * 32, (size_t)warps * 512 * 4, st, a);
+            }
+        if constexpr (G == 128)
+            if (!wide && by_four(8))
+                return launch(w4_kernel<T, G, 2, 1, true, true>, dim3(pairs, gy), 256, (size_t)8 * 256 * 4, st, a);
+    }
+    const unsigned tiles = ((unsigned)a.out + 15) / 16;
     const unsigned long long blocks = (unsigned long long)tiles * gy;
     int warps = blocks < 2ull * sms ? 16 : blocks < 3ull * sms ? 4 : 8;
     while (warps > 4 && warps / 2 >= a.units) warps /= 2;
-    const bool xv = aligned16(a.x) && a.ld_x % 8 == 0, wide = a.m > 8;
-    // where that leaves no warp without work
-    const bool sv = xv && !wide && a.units % 4 == 0 && a.units >= 4 * warps && reinterpret_cast<uintptr_t>(a.qs) % 8 == 0;
     void (*kernel)(W4Args) =
-        wide ? (xv ? w4_kernel<T, G, 2, true, false> : w4_kernel<T, G, 2, false, false>)
-             : (sv ? w4_kernel<T, G, 1, true, true> : xv ? w4_kernel<T, G, 1, true, false> : w4_kernel<T, G, 1, false, false>);
+        wide ? (xv ? w4_kernel<T, G, 1, 2, true, false> : w4_kernel<T, G, 1, 2, false, false>)
+             : (by_four(warps) ? w4_kernel<T, G, 1, 1, true, true>
+                : xv           ? w4_kernel<T, G, 1, 1, true, false>
+                               : w4_kernel<T, G, 1, 1, false, false>);
     return launch(kernel, dim3(tiles, gy), warps * 32, (size_t)warps * (wide ? 256 : 128) * 4, st, a);
 }
 

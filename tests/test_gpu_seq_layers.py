@@ -338,6 +338,16 @@ def test_w4(m, o, k, group, dtype):
     run_w4(m, o, k, group, dtype, seed=m + o)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,o,k,group", [(1, 2435, 4096, 128), (8, 2435, 4096, 128), (5, 4900, 4224, 128),
+                                         (7, 2435, 4064, 128), (9, 2435, 2048, 64), (16, 2435, 4096, 128),
+                                         (12, 4900, 4160, 64), (33, 1217, 4000, 128), (41, 833, 2080, 64)])
+def test_w4_two_tiles_of_outputs(m, o, k, group, dtype):
+    """Enough outputs and inputs for blocks of 32 outputs, with a last block, a last token and a last
+    group that are not whole, and scales that can and cannot be read four at a time."""
+    run_w4(m, o, k, group, dtype, seed=m + o)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "relu6", "silu"])
 @pytest.mark.parametrize("fold", [False, True])
 def test_w4_options(act, fold):
