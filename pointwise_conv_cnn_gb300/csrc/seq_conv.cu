@@ -165,7 +165,10 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
 #pragma unroll
         for (int j = 0; j < H; j++) last[j].store(static_cast<T *>(a.state_out) + at + (size_t)j * a.c);
     }
-    auto compute = [&](int i, int n) {   // rows i .. i + n - 1, loaded
+    // the rows' addresses by addition: a product each would be half of a single channel's instructions
+    const T *from = x + (long long)i0 * a.ld_x;
+    T *to = y + (long long)i0 * a.ld_y;
+    auto compute = [&](int n) {   // the n rows that were loaded
 #pragma unroll
         for (int u = 0; u < U; u++) {
             if (u >= n) break;
@@ -185,7 +188,8 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
             }
             Vec<T, VEC> out;
             out.put(o);
-            *reinterpret_cast<Vec<T, VEC> *>(y + (long long)(i + u) * a.ld_y) = out;
+            *reinterpret_cast<Vec<T, VEC> *>(to) = out;
+            to += a.ld_y;
         }
 #pragma unroll
         for (int j = 0; j < H; j++) win[j] = win[U + j];
@@ -193,16 +197,19 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
     int i = i0;
     for (; i + U <= i1; i += U) {
 #pragma unroll
-        for (int u = 0; u < U; u++) win[H + u].load(x + (long long)(i + u) * a.ld_x);
-        compute(i, U);
+        for (int u = 0; u < U; u++, from += a.ld_x) win[H + u].load(from);
+        compute(U);
     }
     if (i + 1 < i1) {   // the last one again in the place of rows that there are not: no load waits
 #pragma unroll
-        for (int u = 0; u < U; u++) win[H + u].load(x + (long long)min(i + u, i1 - 1) * a.ld_x);
-        compute(i, i1 - i);
+        for (int u = 0; u < U; u++) {
+            win[H + u].load(from);
+            if (i + u + 1 < i1) from += a.ld_x;
+        }
+        compute(i1 - i);
     } else if (i < i1) {
-        win[H].load(x + (long long)i * a.ld_x);
-        compute(i, 1);
+        win[H].load(from);
+        compute(1);
     }
 }
 
