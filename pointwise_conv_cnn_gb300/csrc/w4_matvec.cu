@@ -66,6 +66,15 @@ template <typename T> __device__ __forceinline__ uint32_t two_weights(uint32_t q
 // from memory to the tensor cores as whole numbers, without a detour, and a group's sum is
 // scaled in 32 bits.  XV: x's rows are 16-byte aligned.  SV: four scales are loaded at once, since a
 // load whose lanes read eight rows takes eight turns at the cache whatever it brings.
+//
+// The weights come from memory once: 20480 x 8192 in groups of 128, one token, 86.5 MB in 27.2 us, 3.2
+// TB/s, 0.48 of a plain copy's rate.  What binds is the integer pipe that takes the weights apart (65 %
+// busy: a shift, a mask and a difference each two weights) and, from eight tokens on, the cache's turns
+// for the inputs (16 tokens 42.0 us, 0.77 of the cache's rate).  The warp-wide product is used since its
+// factors come from registers, where the weights are; the larger ones of the tensor cores
+// want them in shared memory, a detour of a store and a barrier for at most 16 columns, and the tensor cores
+// are 20 % busy as it is.  Tried without gain: weights through a ring in shared memory (41 us), staged
+// scales and inputs (38), one persistent block an SM (30 to 34), four tiles of outputs (33).
 template <typename T, int G, int MT, int NT, bool XV, bool SV>
 __global__ void __launch_bounds__(512, MT * NT == 1 ? 2 : 1) w4_kernel(const W4Args a) {
     constexpr int WORDS = G / 32;   // words per lane and group

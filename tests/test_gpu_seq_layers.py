@@ -221,6 +221,31 @@ def test_scan_slots(in_place):
     run_scan([1, 1, 1], 48, 16, "bf16", packed=False, slots=4, slot=[2, 4, 1 << 30], in_place=in_place)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("c,n,groups", [(64, 12, 1), (40, 20, 1), (45, 28, 1), (24, 40, 1), (17, 42, 1),
+                                        (16, 72, 1), (10, 76, 2), (128, 12, 2), (126, 16, 1)])
+@pytest.mark.parametrize("left,right", [(0, 0), (3, 0)])
+def test_scan_odd_states_and_rows(c, n, groups, left, right, dtype):
+    """State counts that leave lanes of a channel empty, or part of one; rows of the channels and
+    of the states that start on 16 bytes or do not, each with the other."""
+    run_scan([33, 0, 70], c, n, dtype, groups, left=left, right=right, seed=c + n)
+
+
+@pytest.mark.parametrize("n", [12, 20, 40])
+def test_scan_infinities_and_empty_lanes(n):
+    """What an infinite input makes of the states that there are does not meet those that there are not."""
+    c, length = 20, 40
+    x = torch.ones((1, length, c), device="cuda")
+    x[0, 5, 3] = float("inf")
+    one = torch.ones((1, length, n), device="cuda")
+    y = torch.empty_like(x)
+    fcm.selective_scan(x, torch.ones_like(x), -0.01 * torch.ones((c, n), device="cuda"), one, one, y,
+                       softplus=False)
+    assert bool((y[0, 5:, 3] == float("inf")).all()) and bool(torch.isfinite(y[0, :5]).all())
+    y[0, :, 3] = 0
+    assert bool(torch.isfinite(y).all())
+
+
 @pytest.mark.parametrize("n", [1, 3, 5, 16])
 @pytest.mark.parametrize("length", [1, 40])
 def test_scan_infinities_stay_where_they_are(n, length):
