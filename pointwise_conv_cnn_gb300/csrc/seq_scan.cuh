@@ -267,15 +267,82 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                 };
                 const int rows = min(TT, t1 - t0 - k * TT);
                 if (rows == TT) {
-#pragma unroll 1
-                    for (int r = 0; r < TT; r += kUnr) {
-                        float sums[kUnr];   // stored together: a store holds up the loads behind it
+                    // Three stages of R rows each: loads, exponentials, and the recurrence; a batch's
+                    // sums are stored behind the next one's loads.
+                    constexpr int R = 16 / SPT, NB = TT / R, H = SPT / 2;
+                    struct In {
+                        float2 s[R];
+                        ulonglong2 b[R][H / 2], c[R][H / 2];
+                    };
+                    struct Mid {
+                        f32x2 e[R][H], u[R][H];
+                    };
+                    auto load = [&](In &x, int r0) {
 #pragma unroll
-                        for (int i = 0; i < kUnr; i++) sums[i] = step(r + i);
-                        if (OUT)
+                        for (int i = 0; i < R; i++) {
+                            x.s[i] = du[(r0 + i) * CH];
 #pragma unroll
-                            for (int i = 0; i < kUnr; i++) out[(r + i) * CH * LPC] = sums[i];
+                            for (int j = 0; j < H / 2; j++) {
+                                x.b[i][j] = *reinterpret_cast<const ulonglong2 *>(bc + (r0 + i) * 2 * NP + 4 * j);
+                                if (OUT) x.c[i][j] = *reinterpret_cast<const ulonglong2 *>(bc + (r0 + i) * 2 * NP + NP + 4 * j);
+                            }
+                        }
+                    };
+                    auto factors = [&](Mid &m, const In &x) {
+#pragma unroll
+                        for (int i = 0; i < R; i++) {
+                            const f32x2 u2 = pack2(x.s[i].y, x.s[i].y), d2 = pack2(x.s[i].x, x.s[i].x);
+                            if (SPLIT && !OUT) sum_d += x.s[i].x;
+#pragma unroll
+                            for (int j = 0; j < H; j++) {
+                                float e0, e1;
+                                unpack2(mul2(d2, av[j]), e0, e1);
+                                m.e[i][j] = pack2(ex2(e0), ex2(e1));
+                                m.u[i][j] = mul2(u2, j & 1 ? x.b[i][j / 2].y : x.b[i][j / 2].x);
+                            }
+                        }
+                    };
+                    auto advance = [&](const Mid &m, const In &x, float (&sums)[R]) {
+#pragma unroll
+                        for (int i = 0; i < R; i++) {
+                            f32x2 acc[2] = {0, 0};
+#pragma unroll
+                            for (int j = 0; j < H; j++) {
+                                h[j] = fma2(m.e[i][j], h[j], m.u[i][j]);
+                                if (OUT) {
+                                    f32x2 v = h[j];
+                                    if (PAD == 2) {
+                                        float p0, p1;
+                                        unpack2(v, p0, p1);
+                                        v = pack2(n0 + 2 * j < a.n ? p0 : 0.0f, n0 + 2 * j + 1 < a.n ? p1 : 0.0f);
+                                    }
+                                    const f32x2 c = j & 1 ? x.c[i][j / 2].y : x.c[i][j / 2].x;
+                                    acc[j & 1] = j < 2 ? mul2(v, c) : fma2(v, c, acc[j & 1]);
+                                }
+                            }
+                            float lo, hi;
+                            unpack2(add2(acc[0], acc[1]), lo, hi);
+                            sums[i] = PAD == 1 && n0 >= a.n ? 0.0f : lo + hi;
+                        }
+                    };
+                    In x[3];
+                    Mid m[2];
+                    float sums[R];
+                    load(x[0], 0);
+                    load(x[1], R);
+                    factors(m[0], x[0]);
+#pragma unroll
+                    for (int k0 = 0; k0 < NB; k0++) {
+                        if (k0 + 2 < NB) load(x[(k0 + 2) % 3], (k0 + 2) * R);
+                        if (OUT && k0 > 0)
+#pragma unroll
+                            for (int i = 0; i < R; i++) out[((k0 - 1) * R + i) * CH * LPC] = sums[i];
+                        if (k0 + 1 < NB) factors(m[(k0 + 1) & 1], x[(k0 + 1) % 3]);
+                        advance(m[k0 & 1], x[k0 % 3], sums);
                     }
+                    if (OUT)
+#pragma unroll
+                        for (int i = 0; i < R; i++) out[((NB - 1) * R + i) * CH * LPC] = sums[i];
                 } else {
 #pragma unroll 1
                     for (int r = 0; r < rows; r++) {
@@ -412,135 +479,145 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
             auto rest = [&](const char *p, long long stride, int r) {
                 return ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)r * (uint32_t)stride) & 15;
             };
-            auto prepare = [&](int k, bool with_c) {
-                const unsigned char *raw = smem + (k % NST) * S::STAGE;
-                if (r0 < RS) {
-                    float x[IT][2], d[IT][2];
-                    if constexpr (vec16) {
+            // PREP: the steps and widened B and C of tile k + 1; OUT: the outputs of tile k - 1.  Everything is
+            // read before anything is written, so that the two tiles' chains run side by side; where there
+            // is no such tile, what lies in its place is worked on and not used.
+            auto serve_tile = [&](auto prep_tag, auto c_tag, auto out_tag, auto gate_tag, int k) {
+                constexpr bool PREP = decltype(prep_tag)::value, WITH_C = decltype(c_tag)::value;
+                constexpr bool OUT = decltype(out_tag)::value, GATE = decltype(gate_tag)::value;
+                const unsigned char *next = smem + (k + 1) % S::NST * S::STAGE;
+                const unsigned char *last = smem + (k + S::NST - 1) % S::NST * S::STAGE;
+                const bool rows_mine = PR * RS == 128 || r0 < RS, quads_mine = QR * QS == 128 || rq < QS;
+                float x[IT][2], d[IT][2], o[IT][2], xo[IT][2], zo[IT][2];
+                float4 v[2][QT];
+                if (PREP && rows_mine) {
 #pragma unroll
-                        for (int i = 0; i < IT; i++) {
-                            const unsigned char *p = raw + (r0 + i * RS) * PITCHX + ch * E;
-                            get_pair<T>(p, true, x[i][0], x[i][1]);
-                            get_pair<T>(p + S::X_BYTES, true, d[i][0], d[i][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < IT; i++) {
-                            const int r = r0 + i * RS;
-                            const unsigned char *p = raw + r * PITCHX + ch * E;
-                            get_pair<T>(p + rest(px, bx, k * TT + r), false, x[i][0], x[i][1]);
-                            get_pair<T>(p + S::X_BYTES + rest(pdt, bdt, k * TT + r), false, d[i][0], d[i][1]);
-                        }
+                    for (int i = 0; i < IT; i++) {
+                        const int r = r0 + i * RS;
+                        const unsigned char *p = next + r * PITCHX + ch * E;
+                        get_pair<T>(p + (vec16 ? 0 : rest(px, bx, (k + 1) * TT + r)), vec16, x[i][0], x[i][1]);
+                        get_pair<T>(p + S::X_BYTES + (vec16 ? 0 : rest(pdt, bdt, (k + 1) * TT + r)), vec16, d[i][0], d[i][1]);
                     }
-#pragma unroll
-                    for (int i = 0; i < IT; i++) d[i][0] += bias[0], d[i][1] += bias[1];
-                    if (a.softplus)
-#pragma unroll
-                        for (int i = 0; i < IT; i++) softplus2(d[i][0], d[i][1]);
-                    float2 *du = at_du(k);
-#pragma unroll
-                    for (int i = 0; i < IT; i++)
-                        *reinterpret_cast<float4 *>(du + (r0 + i * RS) * CH + ch) =
-                            make_float4(d[i][0], d[i][0] * x[i][0], d[i][1], d[i][1] * x[i][1]);
                 }
-                if (rq < QS) {
-                    float *to = at_bc(k);
+                if (PREP && quads_mine) {
 #pragma unroll
-                    for (int which = 0; which < 2; which++) {
-                        if (which && !with_c) break;
-                        const unsigned char *from = raw + 3 * S::X_BYTES + which * S::N_BYTES + n4 * E;
+                    for (int which = 0; which < (WITH_C ? 2 : 1); which++)
 #pragma unroll
                         for (int i = 0; i < QT; i++) {
                             const int r = rq + i * QS;
-                            const unsigned char *p = from + r * PITCHN;
-                            float4 v;
-                            if (!vec16n) p += which ? rest(pc, bc, k * TT + r) : rest(pb, bb, k * TT + r);
-                            get_pair<T>(p, vec16n, v.x, v.y);
-                            get_pair<T>(p + 2 * E, vec16n, v.z, v.w);
+                            const unsigned char *p = next + 3 * S::X_BYTES + which * S::N_BYTES + n4 * E + r * PITCHN;
+                            if (!vec16n) p += which ? rest(pc, bc, (k + 1) * TT + r) : rest(pb, bb, (k + 1) * TT + r);
+                            get_pair<T>(p, vec16n, v[which][i].x, v[which][i].y);
+                            get_pair<T>(p + 2 * E, vec16n, v[which][i].z, v[which][i].w);
+                        }
+                }
+                if (OUT && rows_mine) {
+                    const float *out = at_out(k + 1) + ch * LPC;   // of tile k - 1
+#pragma unroll
+                    for (int i = 0; i < IT; i++) {
+                        const float *p = out + (r0 + i * RS) * CH * LPC;
+                        if constexpr (LPC == 1) {
+                            const float2 w = *reinterpret_cast<const float2 *>(p);
+                            o[i][0] = w.x, o[i][1] = w.y;
+                        } else if constexpr (LPC == 2) {
+                            const float4 w = *reinterpret_cast<const float4 *>(p);
+                            o[i][0] = w.x + w.y, o[i][1] = w.z + w.w;
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 2; c++) {
+                                o[i][c] = 0.0f;
+#pragma unroll
+                                for (int j = 0; j < LPC; j += 4) {
+                                    const float4 w = *reinterpret_cast<const float4 *>(p + c * LPC + j);
+                                    const float sum = (w.x + w.y) + (w.z + w.w);
+                                    o[i][c] = j == 0 ? sum : o[i][c] + sum;
+                                }
+                            }
+                        }
+                        const int r = r0 + i * RS;
+                        const unsigned char *q = last + r * PITCHX + ch * E;
+                        get_pair<T>(q + (vec16 ? 0 : rest(px, bx, (k - 1) * TT + r)), vec16, xo[i][0], xo[i][1]);
+                        if (GATE)
+                            get_pair<T>(q + 2 * S::X_BYTES + (vec16 ? 0 : rest(pz, bz, (k - 1) * TT + r)), vec16, zo[i][0], zo[i][1]);
+                    }
+                }
+                if (rows_mine) {
+                    if (PREP) {
+#pragma unroll
+                        for (int i = 0; i < IT; i++) {
+                            d[i][0] += bias[0], d[i][1] += bias[1];
+                            float p[2] = {d[i][0], d[i][1]};
+                            softplus2(p[0], p[1]);
+                            d[i][0] = a.softplus ? p[0] : d[i][0], d[i][1] = a.softplus ? p[1] : d[i][1];
+                        }
+                    }
+                    if (OUT) {
+#pragma unroll
+                        for (int i = 0; i < IT; i++)
+#pragma unroll
+                            for (int c = 0; c < 2; c++) {
+                                o[i][c] = a.skip ? fmaf(skip[c], xo[i][c], o[i][c]) : o[i][c];
+                                if (GATE) o[i][c] *= silu(zo[i][c]);
+                            }
+                    }
+                    if (PREP) {
+                        float2 *du = at_du(k + 1);
+#pragma unroll
+                        for (int i = 0; i < IT; i++)
+                            *reinterpret_cast<float4 *>(du + (r0 + i * RS) * CH + ch) =
+                                make_float4(d[i][0], d[i][0] * x[i][0], d[i][1], d[i][1] * x[i][1]);
+                    }
+                }
+                if (PREP && quads_mine) {
+                    float *to = at_bc(k + 1);
+#pragma unroll
+                    for (int which = 0; which < (WITH_C ? 2 : 1); which++)
+#pragma unroll
+                        for (int i = 0; i < QT; i++) {
+                            float4 w = v[which][i];
                             if (PAD) {   // padding states: nothing in, nothing out
-                                v.x = n4 < a.n ? v.x : 0.0f, v.y = n4 + 1 < a.n ? v.y : 0.0f;
-                                v.z = n4 + 2 < a.n ? v.z : 0.0f, v.w = n4 + 3 < a.n ? v.w : 0.0f;
+                                w.x = n4 < a.n ? w.x : 0.0f, w.y = n4 + 1 < a.n ? w.y : 0.0f;
+                                w.z = n4 + 2 < a.n ? w.z : 0.0f, w.w = n4 + 3 < a.n ? w.w : 0.0f;
                             }
-                            *reinterpret_cast<float4 *>(to + r * 2 * NP + which * NP + n4) = v;
+                            *reinterpret_cast<float4 *>(to + (rq + i * QS) * 2 * NP + which * NP + n4) = w;
                         }
-                    }
                 }
-            };
-            auto finish = [&](int k) {
-                if (r0 >= RS) return;
-                const unsigned char *raw = smem + (k % NST) * S::STAGE;
-                const float *out = at_out(k) + ch * LPC;
-                float o[IT][2];
+                if (OUT && k > 0 && rows_mine) {
+                    const int left = t1 - t0 - (k - 1) * TT;
 #pragma unroll
-                for (int i = 0; i < IT; i++) {
-                    const float *p = out + (r0 + i * RS) * CH * LPC;
-                    if constexpr (LPC == 1) {
-                        const float2 v = *reinterpret_cast<const float2 *>(p);
-                        o[i][0] = v.x, o[i][1] = v.y;
-                    } else if constexpr (LPC == 2) {
-                        const float4 v = *reinterpret_cast<const float4 *>(p);
-                        o[i][0] = v.x + v.y, o[i][1] = v.z + v.w;
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 2; c++) {
-                            o[i][c] = 0.0f;
-#pragma unroll
-                            for (int j = 0; j < LPC; j += 4) {
-                                const float4 v = *reinterpret_cast<const float4 *>(p + c * LPC + j);
-                                const float s = (v.x + v.y) + (v.z + v.w);
-                                o[i][c] = j == 0 ? s : o[i][c] + s;
-                            }
-                        }
-                    }
+                    for (int i = 0; i < IT; i++)
+                        if (r0 + i * RS < left)
+                            store_pair<T>(py + ((long long)(k - 1) * TT + i * RS) * a.ld_y, o[i][0], o[i][1], have, a.vec2);
                 }
-                if (a.skip)
-#pragma unroll
-                    for (int i = 0; i < IT; i++) {
-                        const int r = r0 + i * RS;
-                        float x, y;
-                        get_pair<T>(raw + r * PITCHX + ch * E + (vec16 ? 0 : rest(px, bx, k * TT + r)), vec16, x, y);
-                        o[i][0] = fmaf(skip[0], x, o[i][0]);
-                        o[i][1] = fmaf(skip[1], y, o[i][1]);
-                    }
-                if (a.z)
-#pragma unroll
-                    for (int i = 0; i < IT; i++) {
-                        const int r = r0 + i * RS;
-                        float x, y;
-                        get_pair<T>(raw + 2 * S::X_BYTES + r * PITCHX + ch * E + (vec16 ? 0 : rest(pz, bz, k * TT + r)), vec16, x, y);
-                        o[i][0] *= silu(x);
-                        o[i][1] *= silu(y);
-                    }
-                const int left = t1 - t0 - k * TT;
-#pragma unroll
-                for (int i = 0; i < IT; i++)
-                    if (r0 + i * RS < left)
-                        store_pair<T>(py + ((long long)k * TT + i * RS) * a.ld_y, o[i][0], o[i][1], have, a.vec2);
             };
             // Tile k is scanned while tile k + 1 is prepared and tile k - 1 finished; tile k + 2 has
             // arrived at the end of that, tile k + 3 is on its way into the place of tile k - 2.
-            auto serve = [&](bool with_out) {
+            auto serve = [&](auto out_tag, auto gate_tag) {
+                constexpr bool OUT = decltype(out_tag)::value;
                 sx = px + rx * bx + qx, sdt = pdt + rx * bdt + qx, sz = pz + rx * bz + qx;
                 sb = pb + rn * bb + qn, sc = pc + rn * bc + qn;
-                for (int k = 0; k < 3; k++) stage(k, with_out);
+                for (int k = 0; k < 3; k++) stage(k, OUT);
                 cp_wait<1>();                       // tiles 0 and 1
                 helpers_sync();
-                if (tiles > 0) prepare(0, with_out);
+                const std::true_type yes;
+                const std::false_type no;
+                if (tiles > 0) serve_tile(yes, out_tag, no, no, -1);
                 __syncthreads();
                 for (int k = 0; k < tiles; k++) {
-                    stage(k + 3, with_out);
-                    if (k + 1 < tiles) prepare(k + 1, with_out);
-                    if (with_out && k > 0) finish(k - 1);
+                    stage(k + 3, OUT);
+                    serve_tile(yes, out_tag, out_tag, gate_tag, k);
                     cp_wait<1>();                   // tile k + 2
                     __syncthreads();
                 }
-                if (with_out && tiles > 0) finish(tiles - 1);
+                if constexpr (OUT)
+                    if (tiles > 0) serve_tile(no, no, out_tag, gate_tag, tiles);
             };
             if constexpr (SPLIT) {
-                if (rank + 1 < parts) serve(false);
+                if (rank + 1 < parts) serve(std::false_type{}, std::false_type{});
                 cluster_sync();
             }
-            serve(true);
+            if (a.z) serve(std::true_type{}, std::true_type{});
+            else serve(std::true_type{}, std::false_type{});
         };
         if (a.vec16 && a.vec16n) help(std::true_type{}, std::true_type{});
         else if (a.vec16) help(std::true_type{}, std::false_type{});
