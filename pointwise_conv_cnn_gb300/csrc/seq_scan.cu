@@ -197,13 +197,14 @@ static cudaError_t run_tokens(const ScanArgs &a, int sms, cudaStream_t st) {
 // Which shape scans, and over how many parts a sequence is split.  More states per thread cost
 // less per state but leave fewer blocks and more serial work; parts run side by side, but all but
 // the last go over their rows twice.  Measured on one GB300, nanoseconds per row of a block that
-// has its SM to itself (t1); two blocks of an SM take 1.68 times that, or twice it where their
-// shared memory only lets one in at a time; splitting costs 1.69 times the rows, and 4 us.
+// has its SM to itself (t1); two blocks of an SM take 1.74 times that, or twice it where their
+// shared memory only lets one in at a time; splitting costs 1.69 times the rows, and 4 us; clusters of
+// eight are put on fewer SMs, so that 16 of them (128 blocks) are pairs already, 12 are not.
 // Against the other shapes and parts, bf16, 16 states, us (4x4, 8x2, 16x1 states x lanes):
-//   1 x 8192 rows x 4096 channels:  whole 282, 464, 857; best split 364 (2), 328 (4), 322 (8)
-//   1 x 8192 x 1024:                whole 282, 464, 856; best split  99 (8), 156 (8), 184 (8)
-//   4 x 2048 x 4096:                whole 233, 187, 216; split from 279
-//   32 x 256 x 4096:                whole 208, 168, 162; split from 270
+//   1 x 8192 rows x 4096 channels:  whole 248, 400, 797; best split 339 (2), 329 (8), 340 (8)
+//   1 x 8192 x 1024:                whole 248, 400, 797; best split  98 (8), 151 (8), 175 (8)
+//   4 x 2048 x 4096:                whole 215, 177, 203; split from 269
+//   32 x 256 x 4096:                whole 199, 160, 157; split from 271
 struct ScanChoice {
     int spt, lpc, parts;
 };
@@ -211,8 +212,8 @@ template <typename T> static ScanChoice choose_scan(const ScanArgs &a, int sms) 
     static constexpr struct {
         int spt, lpc, most, exact;   // states it takes; exact: no fewer
         double t1;
-    } shapes[] = {{4, 1, 4, 0, 80.0},  {4, 2, 8, 0, 50.0},   {4, 4, 16, 0, 34.4}, {8, 2, 16, 1, 56.6},
-                  {16, 1, 16, 1, 104.5}, {4, 8, 32, 0, 36.8}, {8, 4, 32, 1, 47.7}, {8, 8, 64, 0, 50.0},
+    } shapes[] = {{4, 1, 4, 0, 80.0},  {4, 2, 8, 0, 43.1},   {4, 4, 16, 0, 30.3}, {8, 2, 16, 1, 48.9},
+                  {16, 1, 16, 1, 97.3}, {4, 8, 32, 0, 33.5}, {8, 4, 32, 1, 44.0}, {8, 8, 64, 0, 49.3},
                   {8, 16, 128, 0, 60.0}};
     ScanChoice best = {8, 16, 1};
     double least = 1e300;
@@ -224,11 +225,12 @@ template <typename T> static ScanChoice choose_scan(const ScanArgs &a, int sms) 
     for (const auto &s : shapes) {
         if (s.most != most || (s.exact && a.n != s.most)) continue;
         const int ch = 4 * (32 / s.lpc);
-        const double pair = 2 * scan_smem<T>(s.spt, s.lpc) <= 227 * 1024 ? 1.68 : 2.0;
+        const double pair = 2 * scan_smem<T>(s.spt, s.lpc) <= 227 * 1024 ? 1.74 : 2.0;
         for (int parts = 1; parts <= 8; parts *= 2) {
             const double blocks = (double)a.q.n_seq * a.groups * ((a.cpg + ch - 1) / ch) * parts;
             const double load = ceil(blocks * (filled < 1.0 ? filled : 1.0) / (2.0 * sms));
-            const double step = blocks <= sms ? s.t1 : s.t1 * pair * (load > 1.0 ? load : 1.0);
+            const bool alone = parts == 8 ? 4 * blocks <= 3.0 * sms : blocks <= sms;
+            const double step = alone ? s.t1 : s.t1 * pair * (load > 1.0 ? load : 1.0);
             const double ns = parts == 1 ? step * rows : 1.69 * step * rows / parts + 4000.0;
             if (ns < least) least = ns, best = {s.spt, s.lpc, parts};
         }

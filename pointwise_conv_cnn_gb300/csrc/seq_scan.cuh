@@ -149,13 +149,13 @@ template <typename T> __device__ __forceinline__ void store_pair(T *p, float a, 
 // per channel and token: they load, make the steps D and D * x and widen B and C for the tile
 // behind, and sum the parts' products, gate and store the tile before.
 //
-// Bound by latency and issue of the one scanning warp that each scheduler has (two, where two blocks
-// share an SM): a row of four states a lane is two steps' loads, four exponentials and 16 products, 67
-// cycles.  8192 x 4096, 16 states, bf16: 281 us, where its exponentials take 56 at the SM's 32 a clock
-// and its 269 MB 40; 4 x 2048 x 4096, two blocks an SM, 189.  That the scanning warps do nothing but
-// scan gave 447 -> 282; a scan without helpers, or with more or split teams of them, steps loaded a
-// row ahead, two states a lane (403) and single in place of packed products (288) gave nothing.
-// Rows off 16 bytes: 8192 x 4095 370.
+// Bound by latency and issue of the one scanning warp and the one helping warp that each scheduler has
+// (two of each, where two blocks share an SM): 8192 x 4096, 16 states, bf16: 246 us, 58 cycles a row,
+// where its exponentials take 56 us at the SM's 32 a clock and its 269 MB 40; the scanning warps by
+// themselves would take 155. 4 x 2048 x 4096, two blocks an SM, 177; rows off 16 bytes, 8192 x
+// 4095, 343. What gave that: warps that do nothing but scan 447 -> 282, their rows in three
+// stages and the helpers' two tiles side by side 282 -> 246. What gave nothing: more or split teams of helpers,
+// two states a lane (403 against 282) and single in place of packed products (288).
 constexpr int scan_rows(int ch, int np) { return 1024 / ch < 32 ? 1024 / ch : np >= 64 ? 16 : 32; }
 template <typename T, int SPT, int LPC> struct ScanShape {
     static constexpr int NS = 128, NT = 256;     // scanning threads, threads
