@@ -402,7 +402,8 @@ FCM_API fcm_status fcm_causal_conv(const fcm_causal_conv_desc *desc, const void 
  * [c][n_state], skip, dt_bias [c] float32.  skip, z, dt_bias may be NULL: the term, the gate and
  * the bias are left out.  state_in / state_out [slots][c][n_state] float32 hold h before and
  * after; state_in NULL starts from zeros, state_out NULL keeps nothing.  n_state 1 to 128;
- * groups divides c.  Any dt and a are taken; a state grows where D * a > 0. */
+ * groups divides c.  Any dt and a are taken; a state grows where D * a > 0.  One row's factor
+ * exp(D * a) is a float32: below 2^-126 it counts as 0, from 2^128 on as infinity. */
 typedef struct fcm_scan_desc {
     fcm_seqs seqs;
     int c, n_state, groups, dtype, softplus;

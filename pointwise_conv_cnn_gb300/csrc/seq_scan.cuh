@@ -87,6 +87,17 @@ __device__ __forceinline__ float ld_cluster(uint32_t local, int rank) {
     return v;
 }
 
+// Two states carried through a part's rows, whose decays multiply to 2^t, plus what the part makes from
+// zero; third: t / 3.  t may be far outside a float's exponents where h, or the result, is not, and a
+// factor of 0 or infinity would make NaN of an infinite h or of one of 0.  2^(t / 3), cut to normal
+// numbers and multiplied three times, is neither, and still takes any h that is not 0 past either end.
+__device__ __forceinline__ f32x2 carry2(f32x2 h, f32x2 third, f32x2 from_zero) {
+    float lo, hi;
+    unpack2(third, lo, hi);
+    const f32x2 f = pack2(ex2(fminf(fmaxf(lo, -126.0f), 126.0f)), ex2(fminf(fmaxf(hi, -126.0f), 126.0f)));
+    return fma2(mul2(mul2(h, f), f), f, from_zero);
+}
+
 // ------------------------------------------------------------------ copies to shared memory
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -211,18 +222,17 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
         const int cb = (tid >> 5) * CHW + lane % CHW;           // channel in the block
         const bool live = cb < valid;
         const size_t at = (size_t)(c0 + (live ? cb : 0)) * a.n + n0;
-        f32x2 av[SPT / 2], h[SPT / 2];   // decays (base 2), states
-        float h0[SPT];
+        f32x2 av[SPT / 2], h0[SPT / 2], h[SPT / 2];   // decays (base 2), states before, states
         {
-            float v[SPT];
+            float v[SPT], w[SPT];
 #pragma unroll
             for (int i = 0; i < SPT; i++) {
                 const bool in = live && (PAD == 0 || n0 + i < a.n);
                 v[i] = in ? a.a[at + i] * kLog2e : 0.0f;
-                h0[i] = in && row >= 0 && a.state_in ? a.state_in[(size_t)row * a.c * a.n + at + i] : 0.0f;
+                w[i] = in && row >= 0 && a.state_in ? a.state_in[(size_t)row * a.c * a.n + at + i] : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < SPT / 2; i++) av[i] = pack2(v[2 * i], v[2 * i + 1]);
+            for (int i = 0; i < SPT / 2; i++) av[i] = pack2(v[2 * i], v[2 * i + 1]), h0[i] = pack2(w[2 * i], w[2 * i + 1]);
         }
         float sum_d = 0.0f;
         // the tiles, with or without the products with C
@@ -230,13 +240,14 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
             constexpr bool OUT = decltype(out_tag)::value;
             __syncthreads();
             for (int k = 0; k < tiles; k++) {
+                float tile_d = 0.0f;   // the tile's steps by themselves: their sum's error is a short one's
                 const float2 *du = at_du(k) + cb;
                 const float *bc = at_bc(k) + n0;
                 float *out = at_out(k) + cb * LPC + part;
                 auto step = [&](int r) {
                     const float2 s = du[r * CH];
                     const f32x2 u2 = pack2(s.y, s.y), d2 = pack2(s.x, s.x);
-                    if (SPLIT && !OUT) sum_d += s.x;
+                    if (SPLIT && !OUT) tile_d += s.x;
                     f32x2 acc0 = 0, acc1 = 0;
 #pragma unroll
                     for (int j = 0; j < SPT / 2; j += 2) {
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
 #pragma unroll
                         for (int i = 0; i < R; i++) {
                             const f32x2 u2 = pack2(x.s[i].y, x.s[i].y), d2 = pack2(x.s[i].x, x.s[i].x);
-                            if (SPLIT && !OUT) sum_d += x.s[i].x;
+                            if (SPLIT && !OUT) tile_d += x.s[i].x;
 #pragma unroll
                             for (int j = 0; j < H; j++) {
                                 float e0, e1;
@@ -350,12 +361,13 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                         if (OUT) out[r * CH * LPC] = sum;
                     }
                 }
+                if (SPLIT && !OUT) sum_d += tile_d;
                 __syncthreads();
             }
         };
         if constexpr (SPLIT) {
             // Each part but the last runs from zero; a part's start is the state before the first
-            // one, carried through the parts between: h = exp(a * sum of their steps) * h + theirs.
+            // one, carried through the parts between: h = exp(a * sum of their steps) * h + theirs (carry2).
             float *join = reinterpret_cast<float *>(smem + S::SMEM);
 #pragma unroll
             for (int i = 0; i < SPT / 2; i++) h[i] = 0;
@@ -371,17 +383,16 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
             cluster_sync();
             const uint32_t join_at = tc::smem_u32(join);
             for (int p = 0; p < rank; p++) {
-                const float s = ld_cluster(join_at + (SPT * S::NS + tid) * 4, p);
+                const float s = ld_cluster(join_at + (SPT * S::NS + tid) * 4, p) * (1.0f / 3.0f);
 #pragma unroll
-                for (int i = 0; i < SPT; i++) {
-                    float lo, hi;
-                    unpack2(av[i / 2], lo, hi);
-                    h0[i] = fmaf(ex2(s * (i & 1 ? hi : lo)), h0[i], ld_cluster(join_at + (i * S::NS + tid) * 4, p));
-                }
+                for (int i = 0; i < SPT / 2; i++)
+                    h0[i] = carry2(h0[i], mul2(pack2(s, s), av[i]),
+                                   pack2(ld_cluster(join_at + (2 * i * S::NS + tid) * 4, p),
+                                         ld_cluster(join_at + ((2 * i + 1) * S::NS + tid) * 4, p)));
             }
         }
 #pragma unroll
-        for (int i = 0; i < SPT / 2; i++) h[i] = pack2(h0[2 * i], h0[2 * i + 1]);
+        for (int i = 0; i < SPT / 2; i++) h[i] = h0[i];
         scan(std::true_type{});
         if (rank == parts - 1 && row >= 0 && a.state_out && live) {
             float *to = a.state_out + (size_t)row * a.c * a.n + at;
