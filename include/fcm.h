@@ -366,7 +366,9 @@ FCM_API fcm_status fcm_fuse_plan(const fcm_layer *layers, int n_layers, int batc
 /* Which rows form which sequence, and where each sequence's state lies.
  * Without seq_start every sequence has max_len rows and tokens = n_seq * max_len.  With it (int32
  * [n_seq + 1], not decreasing) sequence q has rows seq_start[q] to seq_start[q+1]; max_len is an
- * upper bound of their lengths, and rows past it or outside [0, tokens) are left alone.  A
+ * upper bound of their lengths, and rows past it or outside [0, tokens) are left alone.  Any bound
+ * from the longest length on gives the same results, one past tokens counts as tokens; the closer it
+ * is, the fewer blocks look for rows that there are not, and 1 lets the single tokens' kernel run.  A
  * sequence may be empty: its state passes through.  Rows of no sequence are not written.
  * slot (int32 [n_seq], optional) gives the row of each sequence in the state tensors, which have
  * `slots` rows; without it sequence q uses row q.  A sequence whose slot is outside [0, slots)

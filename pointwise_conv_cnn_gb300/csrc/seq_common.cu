@@ -27,7 +27,8 @@ fcm_status check_seqs(const fcm_seqs &s, bool state, Seqs *out) {
     out->slot = s.slot;
     out->tokens = s.tokens;
     out->n_seq = s.n_seq;
-    out->max_len = s.max_len;
+    // a bound of the lengths that is past all tokens says no more than the tokens do
+    out->max_len = s.seq_start && s.max_len > s.tokens ? (int)s.tokens : s.max_len;
     out->slots = s.slots;
     return FCM_OK;
 }

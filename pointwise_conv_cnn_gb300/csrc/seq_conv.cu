@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
     long long start;
     int len;
     seq_rows(a.q, q, start, len);
-    const int i0 = tile * a.rows, i1 = min(len, i0 + a.rows);
+    const unsigned i0 = (unsigned)tile * a.rows, i1 = min((unsigned)len, i0 + a.rows);   // may pass 2^31 with rows added
     if (tile > 0 && i0 >= i1) return;
     const T *x = static_cast<const T *>(a.x) + d + start * a.ld_x;
     T *y = static_cast<T *>(a.y) + d + start * a.ld_y;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
 #pragma unroll
         for (int j = 0; j < H; j++) win[j] = win[U + j];
     };
-    int i = i0;
+    unsigned i = i0;
     for (; i + U <= i1; i += U) {
 #pragma unroll
         for (int u = 0; u < U; u++, from += a.ld_x) win[H + u].load(from);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
             win[H + u].load(from);
             if (i + u + 1 < i1) from += a.ld_x;
         }
-        compute(i1 - i);
+        compute((int)(i1 - i));
     } else if (i < i1) {
         win[H].load(from);
         compute(1);
@@ -252,12 +252,14 @@ static cudaError_t run_conv(ConvArgs a, int sms, cudaStream_t st) {
     // 51.8; 4096 x 4096 21.3, 18.3, 16.4, 15.8, 20.2; 1024 x 2048 4.1, 3.7, 4.3, 6.7, 10.9; 256 x 1024 2.9, 3.3,
     // 4.4, 6.6, 11.0.  No fewer rows than cached ones: only the first tile's window reaches those.
     const int least = a.k > 5 ? 8 : 4;
+    auto tiles = [&](int rows) { return a.q.max_len / rows + (a.q.max_len % rows != 0); };
+    const long long most = (long long)sms * 192;
     a.rows = 32;
-    while (a.rows > least && all * ((a.q.max_len + a.rows - 1) / a.rows) < (long long)sms * 192) a.rows /= 2;
-    a.tiles = a.q.max_len ? (a.q.max_len + a.rows - 1) / a.rows : 1;
+    while (a.rows > least && all < most && all * tiles(a.rows) < most) a.rows /= 2;
+    a.tiles = a.q.max_len ? tiles(a.rows) : 1;
+    if (all > 0x7FFFFFFFLL * 128 / a.tiles) return cudaErrorInvalidConfiguration;
     a.threads = all * a.tiles;
     const long long blocks = (a.threads + 127) / 128;
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
     return launch(vec == VEC ? pick_conv<T, VEC>(a.k) : vec == 2 ? pick_conv<T, 2>(a.k) : pick_conv<T, 1>(a.k), dim3((unsigned)blocks), 128, 0, st, a);
 }
 

@@ -43,11 +43,12 @@ __global__ void __launch_bounds__(128, 6) scan_token_kernel(const TokenArgs a) {
     tc::pdl_wait();
     tc::pdl_launch_dependents();
     const int n0 = 4 * (threadIdx.x % LPC), ch = threadIdx.x / LPC;
-    const int d0 = (int)(blockIdx.x % a.blocks) * CHANS, d = min(d0 + ch, a.c - 1);
-    const bool live = d0 + ch < a.c, some = a.q.tokens > 0, mine = VEC ? n0 < a.n : true;
+    const unsigned channels = a.c, d0 = blockIdx.x % a.blocks * CHANS;   // past 2^31 with a block's added
+    const int d = (int)min(d0 + ch, channels - 1);
+    const bool live = d0 + ch < channels, some = a.q.tokens > 0, mine = VEC ? n0 < a.n : true;
     const int last = (int)a.q.tokens - 1;
     // the sequence and channel whose step this thread makes
-    const int pu = min((int)threadIdx.x / CHANS, U - 1), pd = min(d0 + (int)threadIdx.x % CHANS, a.c - 1);
+    const int pu = min((int)threadIdx.x / CHANS, U - 1), pd = (int)min(d0 + threadIdx.x % CHANS, channels - 1);
     const bool makes = (int)threadIdx.x < U * CHANS;
     const float bias = a.dt_bias ? a.dt_bias[pd] : 0.0f, skip = a.skip ? a.skip[pd] : 0.0f;
 
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(128, 6) scan_token_kernel(const TokenArgs a) {
 template <typename T, int LPC>
 static cudaError_t launch_tokens(TokenArgs t, int sms, bool vec, cudaStream_t st) {
     constexpr int CHANS = 128 / LPC;
-    t.blocks = (t.c + CHANS - 1) / CHANS;
+    t.blocks = (t.c - 1) / CHANS + 1;
     // A few blocks for each place an SM has, or as many as there are pairs.  Measured, us with 3, 6, 12, 24,
     // 48 blocks an SM: 192 x 5120 67.6, 36.5, 33.7, 35.6, 38.4; 64 x 4096 12.7, 9.8, 9.7, 11.5, 11.9; 160 x 1536 11.3, 8.5,
     // 9.2, 11.1, 11.2.
@@ -227,7 +228,7 @@ template <typename T> static ScanChoice choose_scan(const ScanArgs &a, int sms) 
         const int ch = 4 * (32 / s.lpc);
         const double pair = 2 * scan_smem<T>(s.spt, s.lpc) <= 227 * 1024 ? 1.74 : 2.0;
         for (int parts = 1; parts <= 8; parts *= 2) {
-            const double blocks = (double)a.q.n_seq * a.groups * ((a.cpg + ch - 1) / ch) * parts;
+            const double blocks = (double)a.q.n_seq * a.groups * ((a.cpg - 1) / ch + 1) * parts;
             const double load = ceil(blocks * (filled < 1.0 ? filled : 1.0) / (2.0 * sms));
             const bool alone = parts == 8 ? 4 * blocks <= 3.0 * sms : blocks <= sms;
             const double step = alone ? s.t1 : s.t1 * pair * (load > 1.0 ? load : 1.0);

@@ -209,9 +209,10 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
     const int valid = min(CH, a.cpg - block * CH);              // the block's channels
     const long long c0 = (long long)g * a.cpg + block * CH;     // the first one
     // this part's rows
-    const int per = SPLIT ? ((len + parts - 1) / parts + TT - 1) / TT * TT : len;
-    const int t0 = SPLIT ? min(len, rank * per) : 0, t1 = SPLIT ? min(len, t0 + per) : len;
-    const int tiles = (t1 - t0 + TT - 1) / TT;
+    const unsigned all = (unsigned)len;   // sums with it may pass 2^31
+    const unsigned per = SPLIT ? ((all + parts - 1) / parts + TT - 1) / TT * TT : all;
+    const int t0 = SPLIT ? (int)min(all, rank * per) : 0, t1 = SPLIT ? (int)min(all, t0 + per) : len;
+    const int tiles = (int)(((unsigned)(t1 - t0) + TT - 1) / TT);
     auto at_du = [&](int k) { return reinterpret_cast<float2 *>(smem + S::NST * S::STAGE + (k & 1) * S::DU); };
     auto at_bc = [&](int k) { return reinterpret_cast<float *>(smem + S::NST * S::STAGE + 2 * S::DU + (k & 1) * S::BC); };
     auto at_out = [&](int k) { return reinterpret_cast<float *>(smem + S::NST * S::STAGE + 2 * (S::DU + S::BC) + (k & 1) * S::OUT); };
@@ -487,8 +488,8 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                 }
             T *py = static_cast<T *>(a.y) + (first + r0) * a.ld_y + c0 + ch;
             // where row r of a tile starts within its place: the copies keep the address's rest
-            auto rest = [&](const char *p, long long stride, int r) {
-                return ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)r * (uint32_t)stride) & 15;
+            auto rest = [&](const char *p, long long stride, uint32_t r) {
+                return ((uint32_t)reinterpret_cast<uintptr_t>(p) + r * (uint32_t)stride) & 15;
             };
             // PREP: the steps and widened B and C of tile k + 1; OUT: the outputs of tile k - 1.  Everything is
             // read before anything is written, so that the two tiles' chains run side by side; where there
@@ -506,8 +507,8 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                     for (int i = 0; i < IT; i++) {
                         const int r = r0 + i * RS;
                         const unsigned char *p = next + r * PITCHX + ch * E;
-                        get_pair<T>(p + (vec16 ? 0 : rest(px, bx, (k + 1) * TT + r)), vec16, x[i][0], x[i][1]);
-                        get_pair<T>(p + S::X_BYTES + (vec16 ? 0 : rest(pdt, bdt, (k + 1) * TT + r)), vec16, d[i][0], d[i][1]);
+                        get_pair<T>(p + (vec16 ? 0 : rest(px, bx, (k + 1u) * TT + r)), vec16, x[i][0], x[i][1]);
+                        get_pair<T>(p + S::X_BYTES + (vec16 ? 0 : rest(pdt, bdt, (k + 1u) * TT + r)), vec16, d[i][0], d[i][1]);
                     }
                 }
                 if (PREP && quads_mine) {
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                         for (int i = 0; i < QT; i++) {
                             const int r = rq + i * QS;
                             const unsigned char *p = next + 3 * S::X_BYTES + which * S::N_BYTES + n4 * E + r * PITCHN;
-                            if (!vec16n) p += which ? rest(pc, bc, (k + 1) * TT + r) : rest(pb, bb, (k + 1) * TT + r);
+                            if (!vec16n) p += which ? rest(pc, bc, (k + 1u) * TT + r) : rest(pb, bb, (k + 1u) * TT + r);
                             get_pair<T>(p, vec16n, v[which][i].x, v[which][i].y);
                             get_pair<T>(p + 2 * E, vec16n, v[which][i].z, v[which][i].w);
                         }
@@ -547,9 +548,9 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                         }
                         const int r = r0 + i * RS;
                         const unsigned char *q = last + r * PITCHX + ch * E;
-                        get_pair<T>(q + (vec16 ? 0 : rest(px, bx, (k - 1) * TT + r)), vec16, xo[i][0], xo[i][1]);
+                        get_pair<T>(q + (vec16 ? 0 : rest(px, bx, (k - 1u) * TT + r)), vec16, xo[i][0], xo[i][1]);
                         if (GATE)
-                            get_pair<T>(q + 2 * S::X_BYTES + (vec16 ? 0 : rest(pz, bz, (k - 1) * TT + r)), vec16, zo[i][0], zo[i][1]);
+                            get_pair<T>(q + 2 * S::X_BYTES + (vec16 ? 0 : rest(pz, bz, (k - 1u) * TT + r)), vec16, zo[i][0], zo[i][1]);
                     }
                 }
                 if (rows_mine) {
@@ -649,9 +650,10 @@ cudaError_t launch_scan_shape(ScanArgs a, int parts, cudaStream_t st) {
     typedef ScanShape<T, SPT, LPC> S;
     static_assert(S::SMEM == scan_smem<T>(SPT, LPC), "");
     static std::atomic<unsigned long long> attr_ctx[2];
-    a.blocks = (a.cpg + S::CH - 1) / S::CH;
-    const long long grid = (long long)a.q.n_seq * a.groups * a.blocks * parts;
-    if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+    a.blocks = (a.cpg - 1) / S::CH + 1;
+    const long long sequences = (long long)a.q.n_seq * a.groups * a.blocks;   // below 2^61
+    if (sequences > 0x7FFFFFFFLL / parts) return cudaErrorInvalidConfiguration;
+    const long long grid = sequences * parts;
     const int smem = S::SMEM + (parts > 1 ? S::JOIN : 0);
     void (*kernel)(ScanArgs) = parts > 1 ? scan_kernel<T, SPT, LPC, PAD, true>
                                          : scan_kernel<T, SPT, LPC, PAD, false>;
