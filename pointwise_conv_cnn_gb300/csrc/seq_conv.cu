@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(128) causal_conv_kernel(const ConvArgs a) {
                 for (int v = 0; v < VEC; v++) o[v] = silu(o[v]);
             } else {
 #pragma unroll
-                for (int v = 0; v < VEC; v++) o[v] = act_apply(o[v], a.act);
+                for (int v = 0; v < VEC; v++) o[v] = clamp_act(o[v], a.act);
             }
             Vec<T, VEC> out;
             out.put(o);
