@@ -422,8 +422,8 @@ FCM_API fcm_status fcm_selective_scan(const fcm_scan_desc *desc, const void *x, 
  *     y[t,o] = act(s[o] * sum_k x[t,k] * qs[o,k/group] * (q[o,k] - 8) + b[o])
  * x [m][in], y [m][out]; qw [out][in/2] bytes, q of an even k in the low four bits of byte k/2 and
  * the next k's in the high four; qs [out][ceil(in/group)] in the storage dtype; s and b [out]
- * float32 (NULL: 1, 0).  in is a multiple of 32 up to 32768, group 32, 64 or 128 (the last group may
- * be short).  The weights are read once for every 16 rows of x. */
+ * float32 (NULL: 1, 0).  in is a multiple of 32, group 32, 64 or 128 (the last group may be
+ * short).  The weights are read once for every 16 rows of x. */
 typedef struct fcm_w4_desc {
     int m, out, in, group, dtype, act;
     long long ld_x, ld_y;

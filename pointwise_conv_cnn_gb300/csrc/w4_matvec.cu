@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(512, MT * NT == 1 ? 2 : 1) w4_kernel(const W4A
         }
     }
     for (; u < u1; u++) {
-        const bool in = u * G + t * (G / 4) < a.in;   // a short group ends with a lane's quarter
+        const bool in = (unsigned)u * G + t * (G / 4) < (unsigned)a.in;   // a short group ends with a lane's quarter
         Weights q = {};
         Inputs v = {};                                // whose inputs past the end are zeros
         if (in) {
@@ -321,7 +321,7 @@ extern "C" fcm_status fcm_w4_matvec(const fcm_w4_desc *desc, const void *x, cons
     if ((st = seq::current_device(&sms)) != FCM_OK) return st;
 
     const seq::W4Args a = {x, qw, qs, s, b, y, d.ld_x, d.ld_y, d.m, d.out, d.in, d.act,
-                           (d.in + d.group - 1) / d.group};
+                           (d.in - 1) / d.group + 1};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t ce;
     if (d.dtype == FCM_F16)
