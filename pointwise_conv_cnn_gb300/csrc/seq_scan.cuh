@@ -26,7 +26,6 @@ struct ScanArgs {
     int vec2;       // every block's row of y starts on two elements
 };
 
-constexpr int kUnr = 8;   // steps whose sums are stored together
 constexpr int kMaxState = 128;
 
 // ------------------------------------------------------------------ arithmetic
@@ -190,7 +189,6 @@ template <typename T, int SPT, int LPC, int PAD, bool SPLIT>
 __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
     typedef ScanShape<T, SPT, LPC> S;
     constexpr int TT = S::TT, CH = S::CH, CHW = S::CHW, NP = S::NP;
-    static_assert(TT % kUnr == 0, "a batch of steps stays in its tile");
     extern __shared__ __align__(16) unsigned char smem[];
 
     tc::pdl_wait();
@@ -282,6 +280,9 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(const ScanArgs a) {
                     // Three stages of R rows each: loads, exponentials, and the recurrence; a batch's
                     // sums are stored behind the next one's loads.
                     constexpr int R = 16 / SPT, NB = TT / R, H = SPT / 2;
+                    static_assert(R * SPT == 16 && NB * R == TT, "batches fill the tile");
+                    static_assert(NB >= 2, "two batches are loaded before the first is used");
+                    static_assert(SPT % 4 == 0, "a lane's part of B and C is whole 16-byte loads");
                     struct In {
                         float2 s[R];
                         ulonglong2 b[R][H / 2], c[R][H / 2];
