@@ -359,7 +359,8 @@ FCM_API fcm_status fcm_fuse_plan(const fcm_layer *layers, int n_layers, int batc
  *    16-byte aligned pointers and row distances run fastest; any others are served.
  *  - dtype is FCM_F32, FCM_F16 or FCM_BF16 (fcm_w4_matvec: the last two).  Products, sums,
  *    states of the scan, exponentials and activations are float32; each output is rounded once.
- *    NaN goes through every activation (the fused modules' ReLU and ReLU6 make it 0).
+ *    NaN goes through every activation (the fused modules' ReLU and ReLU6 make it 0).  silu(v) is -0
+ *    for v below -87.34, where its magnitude is 1.03e-36 at most.
  *  - Outputs must not overlap inputs, except that state_out may be state_in itself.
  *  - Kernels are launched with programmatic stream serialization allowed, as fcm_run's are.
  *  - Results do not depend on the launch: the same bits on every run on the same device. */

@@ -47,8 +47,10 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
-// v / (1 + e^-v).  Where e^-v is infinite, or its reciprocal below the least normal number, the
-// result is -0, the limit.
+// v / (1 + e^-v).  Where the reciprocal of the sum is below the least normal number, from v = -87.34 down,
+// the result is -0, its limit; no result that is lost is above 1.03e-36.  Keeping them (e^-v as a square of
+// e^(-v/2), the sum held in range by 2^-32) cost the convolution of 16384 x 4096 1 us of 50.6, of 16384 x 4095
+// 2.5 of 67.6, the scan of 4 x 2048 x 4096 2.3 of 175.7.
 __device__ __forceinline__ float silu(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(-kLog2e * v)));
