@@ -25,6 +25,7 @@ import pointwise_conv_cnn_gb300 as fcm  # noqa: E402
 DTYPE = torch.bfloat16
 GROUP = 32
 FEW = 16   # rows up to which the 4-bit product is used
+LEAST, MOST = 64, 4096   # rows of the pointwise convolutions that a layer keeps: the powers of two between
 
 
 def quantise(w: torch.Tensor):
@@ -48,7 +49,7 @@ class Pointwise:
     def __init__(self, w: torch.Tensor):
         self.qw, self.scale = (t.contiguous() for t in quantise(w))
         self.out, self.inp = w.shape
-        self.modules = {}   # the pointwise convolution for each prompt length met
+        self.modules = {}   # the pointwise convolution for each piece of a prompt
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
         rows = x.shape[0]
@@ -56,14 +57,29 @@ class Pointwise:
         if rows <= FEW:
             fcm.w4_matvec(x, self.qw, self.scale, y, GROUP)
             return y
+        # A convolution is planned for its rows.  A prompt goes through in pieces of powers of two, the last one
+        # filled up, so that a layer keeps a handful of them whatever lengths it meets.
+        x, at = x.contiguous(), 0
+        while rows - at >= LEAST:
+            n = min(MOST, 1 << ((rows - at).bit_length() - 1))
+            self.module(n).run(x[at:at + n], y[at:at + n], "pw")
+            at += n
+        if at < rows:
+            piece = torch.zeros((LEAST, self.inp), dtype=DTYPE, device=x.device)
+            piece[:rows - at] = x[at:]
+            out = torch.empty((LEAST, self.out), dtype=DTYPE, device=x.device)
+            self.module(LEAST).run(piece, out, "pw")
+            y[at:] = out[:rows - at]
+        return y
+
+    def module(self, rows: int) -> fcm.FusedConvModule:
         if rows not in self.modules:
             one, zero = torch.ones(max(self.out, self.inp)), torch.zeros(max(self.out, self.inp))
             desc = fcm.make_desc(n=1, h=1, w=rows, c=self.inp, k_out=self.out, ksize=1, stride=1, pad=0,
                                  conv1="dw", dtype="bf16", act1="none", act2="none")
             self.modules[rows] = fcm.FusedConvModule(
                 desc, torch.ones(self.inp, dtype=DTYPE), widen(self.qw, self.scale).cpu(), one, zero, one, zero)
-        self.modules[rows].run(x.contiguous(), y, "pw")
-        return y
+        return self.modules[rows]
 
 
 class SsmBlock:
