@@ -245,11 +245,19 @@ __global__ void __launch_bounds__(512, MT * NT == 1 ? 2 : 1) w4_kernel(const W4A
 // (5120 x 1024 3.7 and 4.3), and up to 8 tokens scales that are not loaded by four (5120 x 5120, 1 token
 // 7.1 and 7.7).
 //
-// More warps share the inputs where the tiles leave SMs without a block, fewer where most SMs hold
-// two blocks and some a third.  Measured, us with 16, 8 and 4 warps, one tile: 3600 x 4096 in groups of 64 (225
-// blocks), 8 tokens 5.0, 4.8, 5.6; 2048 x 4096 (128) 3.2, 3.5, 4.8; 5003 x 4096 in groups of 32 (313) 7.5,
-// 7.9, 6.5; 16384 x 4096 in groups of 64 (1024) 12.9, 12.0, 13.6; two tiles, 16 tokens: 4096 x 4096 (128) 6.9, 7.2, 7.8;
-// 8192 x 8192 (256) 18.5, 17.2, 18.1.
+// More warps share the inputs where the tiles leave SMs without a block, fewer where every SM has several.
+// Measured for one tile with weights that come from memory, us with 16, 8 and 4 warps, 18 output counts from 2000
+// to 16384 each:
+//   over 8 tokens, where a block of 16 warps has its SM to itself: 8 from the second block an SM on, but 4 from 2
+//     to 2.4.  In groups of 32, 16 tokens: 2432 x 4096 (152 blocks) 6.6, 7.1, 9.6; 3600 x 4096 (225) 11.4, 9.3, 11.0; x 8192
+//     17.8, 15.9, 18.7; 5600 x 4096 (350) 15.9, 14.4, 13.0; 6144 x 4096 (384) 16.0, 15.4, 19.1; x 2048 10.9, 9.4, 10.9;
+//     13000 x 4096 (813) 29.8, 24.8, 27.5.
+//   up to 8 tokens, fewer than two blocks an SM: 16.  3600 x 2048 in groups of 32, 8 tokens 4.7, 4.4, 5.1; 3600 x 4096 in
+//     groups of 64, 1 token 5.6, 5.7, 7.9; x 8192 8.5, 9.5, 13.8.
+//   two to three: 4, and 16 for long sums, where 4 do not keep enough loads under way.  Groups of 32, 1 token: 5003 x
+//     2048 6.0, 5.5, 5.2; x 4096 8.8, 8.8, 8.4; x 8192 13.5, 15.3, 14.6.  Groups of 64: x 2048 5.5, 5.3, 5.1; x 8192 12.1, 14.1,
+//     14.4; x 4096 7.4, 8.2, 8.4 from memory, but from the L2 6.3 with 16 and 6.1 with 4, 8 tokens 6.9 and 6.6.
+//   more: 8.  16384 x 4096 in groups of 64, 1 token 15.7, 13.6, 14.7.
 template <typename T, int G>
 static cudaError_t run_w4(const W4Args &a, int sms, cudaStream_t st) {
     const bool xv = aligned16(a.x) && a.ld_x % 8 == 0, wide = a.m > 8;
@@ -274,7 +282,11 @@ static cudaError_t run_w4(const W4Args &a, int sms, cudaStream_t st) {
     }
     const unsigned tiles = ((unsigned)a.out + 15) / 16;
     const unsigned long long blocks = (unsigned long long)tiles * gy;
-    int warps = blocks < 2ull * sms ? 16 : blocks < 3ull * sms ? 4 : 8;
+    const unsigned long long n = (unsigned long long)sms;
+    int warps = 8;
+    if (blocks <= n || (!wide && blocks < 2 * n)) warps = 16;
+    else if (wide && blocks >= 2 * n && 5 * blocks <= 12 * n) warps = 4;
+    else if (!wide && blocks < 3 * n) warps = a.in < 8192 ? 4 : 16;
     while (warps > 4 && warps / 2 >= a.units) warps /= 2;
     void (*kernel)(W4Args) =
         wide ? (xv ? w4_kernel<T, G, 1, 2, true, false> : w4_kernel<T, G, 1, 2, false, false>)
