@@ -353,7 +353,9 @@ FCM_API fcm_status fcm_fuse_plan(const fcm_layer *layers, int n_layers, int batc
  *  - Every pointer but the descriptor is device memory owned by the caller, aligned to its
  *    element (qw of fcm_w4_matvec: 16 bytes); the calls run on the current device, enqueue on
  *    `stream` and return.  What the host cannot see (seq_start, slot) is bounded by the kernels
- *    as said below: no value in them makes a kernel read or write outside the tensors described.
+ *    as said below: no value in them makes a kernel read or write outside the tensors described
+ *    (but for the bytes before a row in the aligned 16-byte piece that it starts in, 14 at most,
+ *    which the scan loads and does not use).
  *  - Activations are rows of channels, one row per token, `ld_*` elements apart (0: the row's
  *    own length, rows contiguous), so a layer reads and writes column blocks of wider tensors.
  *    16-byte aligned pointers and row distances run fastest; any others are served.

@@ -202,9 +202,9 @@ static cudaError_t run_tokens(const ScanArgs &a, int sms, cudaStream_t st) {
 // shared memory only lets one in at a time; splitting costs 1.69 times the rows, and 4 us; clusters of
 // eight are put on fewer SMs, so that 16 of them (128 blocks) are pairs already, 12 are not.
 // Against the other shapes and parts, bf16, 16 states, us (4x4, 8x2, 16x1 states x lanes):
-//   1 x 8192 rows x 4096 channels:  whole 248, 400, 797; best split 339 (2), 329 (8), 340 (8)
-//   1 x 8192 x 1024:                whole 248, 400, 797; best split  98 (8), 151 (8), 175 (8)
-//   4 x 2048 x 4096:                whole 215, 177, 203; split from 269
+//   1 x 8192 rows x 4096 channels:  whole 245, 400, 797; best split 339 (2), 329 (8), 340 (8)
+//   1 x 8192 x 1024:                whole 245, 400, 797; best split  98 (8), 151 (8), 175 (8)
+//   4 x 2048 x 4096:                whole 215, 176, 203; split from 269
 //   32 x 256 x 4096:                whole 199, 160, 157; split from 271
 struct ScanChoice {
     int spt, lpc, parts;

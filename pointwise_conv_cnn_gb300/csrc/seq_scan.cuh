@@ -109,7 +109,8 @@ template <int N> __device__ __forceinline__ void cp_wait() {
 // A tile's rows lie 16 bytes further apart than their length, which keeps lanes that read different
 // rows on different banks.  16-byte aligned rows are copied in 16-byte pieces; others in the
 // aligned pieces that hold their bytes, each row at the offset that its address has within a
-// piece (an allocation starts on a piece, and of the last piece no more than the row is read).
+// piece (an allocation starts on a piece, so that the bytes before the row are mapped; of the last
+// piece no more than the row is read).
 // What lies past a tile's rows or a row's elements is not used.
 constexpr int row_pitch(int rb) { return (rb < 16 ? 16 : rb) + 16; }
 // A barrier of the four warps that do not scan.
@@ -159,13 +160,14 @@ template <typename T> __device__ __forceinline__ void store_pair(T *p, float a, 
 // per channel and token: they load, make the steps D and D * x and widen B and C for the tile
 // behind, and sum the parts' products, gate and store the tile before.
 //
-// Bound by latency and issue of the one scanning warp and the one helping warp that each scheduler has
-// (two of each, where two blocks share an SM): 8192 x 4096, 16 states, bf16: 246 us, 58 cycles a row,
-// where its exponentials take 56 us at the SM's 32 a clock and its 269 MB 40; the scanning warps by
-// themselves would take 155. 4 x 2048 x 4096, two blocks an SM, 177; rows off 16 bytes, 8192 x
-// 4095, 343. What gave that: warps that do nothing but scan 447 -> 282, their rows in three
-// stages and the helpers' two tiles side by side 282 -> 246. What gave nothing: more or split teams of helpers,
-// two states a lane (403 against 282) and single in place of packed products (288).
+// Bound by shared memory (its pipe is 76 % busy: steps, widened B and C, partial sums) and by the latencies
+// of the one scanning warp and the one helping warp that each scheduler has (two of each, where two blocks share
+// an SM; issue is at 49 %): 8192 x 4096, 16 states, bf16: 245 us, 58 cycles a row, where its exponentials
+// take 56 us at the SM's 32 a clock and its 269 MB 40; the scanning warps by themselves would take 155.
+// 4 x 2048 x 4096, two blocks an SM, 176; rows off 16 bytes, 8192 x 4095, 344. What gave that: warps that do
+// nothing but scan 447 -> 282, their rows in three stages and the helpers' two tiles side by side 282 -> 249.
+// What gave nothing: more or split teams of helpers, two states a lane (403 against 282) and single in place of
+// packed products (288).
 constexpr int scan_rows(int ch, int np) { return 1024 / ch < 32 ? 1024 / ch : np >= 64 ? 16 : 32; }
 template <typename T, int SPT, int LPC> struct ScanShape {
     static constexpr int NS = 128, NT = 256;     // scanning threads, threads

@@ -39,8 +39,9 @@ __device__ __forceinline__ uint4 load_if(const void *p, bool yes) {
     return v;
 }
 
-// The values of bits [4j, 4j + 4) and [4j + 16, 4j + 20) of q, less 8, in two halves: the bits are
-// put into the mantissa of 1024 (f16) or 128 (bf16), so that the difference is exact.  f16's
+// The values of bits [4j, 4j + 4) and [4j + 16, 4j + 20) of q, less 8, in two halves.  The long known
+// conversion of small whole numbers without an instruction for it: the bits are put into the mantissa
+// of a power of two whose last place is 1, 1024 (f16) or 128 (bf16), which the difference takes out exactly.  f16's
 // mantissa has room for them four places up as well, which saves shifts: 1024 + 16 q is scaled back.
 template <typename T> __device__ __forceinline__ uint32_t two_weights(uint32_t q, int j) {
     uint32_t r;
@@ -69,10 +70,10 @@ template <typename T> __device__ __forceinline__ uint32_t two_weights(uint32_t q
 // scaled in 32 bits.  XV: x's rows are 16-byte aligned.  SV: four scales are loaded at once, since a
 // load whose lanes read eight rows takes eight turns at the cache whatever it brings.
 //
-// The weights come from memory once: 20480 x 8192 in groups of 128, one token, 86.5 MB in 27.2 us, 3.2
-// TB/s, 0.48 of a plain copy's rate.  What binds is the integer pipe that takes the weights apart (65 %
+// The weights come from memory once: 20480 x 8192 in groups of 128, one token, 86.5 MB in 27.3 us, 3.2
+// TB/s, 0.47 of a plain copy's rate.  What binds is the integer pipe that takes the weights apart (65 %
 // busy: a shift, a mask and a difference each two weights) and, from eight tokens on, the cache's turns
-// for the inputs (16 tokens 42.0 us, 0.77 of the cache's rate).  The warp-wide product is used since its
+// for the inputs (16 tokens 42.1 us, 0.77 of the cache's rate).  The warp-wide product is used since its
 // factors come from registers, where the weights are; the larger ones of the tensor cores
 // want them in shared memory, a detour of a store and a barrier for at most 16 columns, and the tensor cores
 // are 20 % busy as it is.  Tried without gain: weights through a ring in shared memory (41 us), staged
@@ -238,12 +239,14 @@ __global__ void __launch_bounds__(512, MT * NT == 1 ? 2 : 1) w4_kernel(const W4A
 // One tile of 16 outputs a block or two.  Two halve the reads of the inputs, which with eight and
 // more tokens cost more than the weights' (a warp's 16 rows of weights in a group of 128 are 16 turns
 // at the cache, eight tokens' inputs 64), and their blocks need fewer rounds; one gives more
-// blocks and shorter ones.  Measured, us with one and two: 20480 x 8192 in groups of 128, 1, 8, 16 tokens
-// 28.0, 34.2, 61.6 and 27.5, 28.6, 42.0; 8192 x 8192 13.1, 15.0, 25.0 and 11.0, 12.0, 16.5; 16384 x
-// 4096 in groups of 64, 1, 8, 16 tokens 11.9, 12.4, 22.4 and 13.0, 13.9, 17.3.  One tile: groups of 32 (5003 x
-// 4096, 16 tokens 12.4 and 13.9), fewer blocks than half the SMs (2048 x 4096 5.2 and 6.7), short sums
-// (5120 x 1024 3.7 and 4.3), and up to 8 tokens scales that are not loaded by four (5120 x 5120, 1 token
-// 7.1 and 7.7).
+// blocks and shorter ones.  Measured, weights from memory, us with one and two: 20480 x 8192 in groups of 128, 1, 8,
+// 16 tokens 27.8, 34.3, 61.9 and 27.3, 28.6, 42.4; 8192 x 8192 14.3, 15.1, 26.0 and 12.9, 13.2, 17.6; 4096 x 4096
+// 5.3, 5.9, 8.2 and 5.6, 6.0, 7.1 (from the L2 4.8, 5.9, 8.2 and 4.6, 4.9, 7.0); 16384 x 4096 in groups of 64, 16
+// tokens 23.7 and 19.1.  One tile: groups of 32 (5003 x 4096, 16 tokens 12.4 and 13.9), fewer blocks than half the
+// SMs (2048 x 4096, 1, 8, 16 tokens 4.0, 4.4, 6.0 and 5.2, 5.4, 6.7), short sums (5120 x 1024, 16 tokens 4.4 and 4.7), and up to
+// 8 tokens groups of 64, and scales that are not loaded by four (5120 x 5120, 1 token from the L2 7.1 and 7.7).
+// Two tiles have 16 warps up to a block an SM, else 8.  16 tokens, us with 16, 8 and 4: 4096 x 4096 (128 blocks) 7.1, 8.5,
+// 11.9; 5200 x 4096 in groups of 64 (163) 12.1, 10.6, 12.7; 8192 x 8192 (256) 20.0, 17.6, 21.8.
 //
 // More warps share the inputs where the tiles leave SMs without a block, fewer where every SM has several.
 // Measured for one tile with weights that come from memory, us with 16, 8 and 4 warps, 18 output counts from 2000
@@ -261,8 +264,10 @@ __global__ void __launch_bounds__(512, MT * NT == 1 ? 2 : 1) w4_kernel(const W4A
 template <typename T, int G>
 static cudaError_t run_w4(const W4Args &a, int sms, cudaStream_t st) {
     const bool xv = aligned16(a.x) && a.ld_x % 8 == 0, wide = a.m > 8;
-    // Scales by four, where that leaves the warps' shares nearly alike: 5120 x 5120 in groups of 128, 40 of
-    // them, 4 warps: 8.3 us by four, 7.1 one by one; 5003 x 4096 in groups of 32, 128 of them: 6.5, 8.5.
+    // Scales by four, where that leaves the warps' shares nearly alike.  Measured, weights from memory, us by four and one
+    // by one: 5003 x 4096 in groups of 32 (128 of them, 4 warps), 1 and 7 tokens 8.4, 9.3 and 9.9, 10.7; 20480 x 8192 in
+    // groups of 32 34.1 and 47.7; 5120 x 5120 in groups of 128 (40 of them, 4 warps) 10.5 and 9.5; 2048 x 4096 (32, 16
+    // warps) 4.8 and 3.9.
     auto by_four = [&](int warps) {
         const long long per = (a.units + 4 * warps - 1) / (4 * warps) * 4;
         return xv && a.units % 4 == 0 && reinterpret_cast<uintptr_t>(a.qs) % 8 == 0 && per * warps * 8 <= a.units * 9ll;
