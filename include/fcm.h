@@ -345,13 +345,13 @@ FCM_API fcm_status fcm_fuse_plan(const fcm_layer *layers, int n_layers, int batc
                                  int num_sms, long long l1_bytes, int elem_bytes,
                                  fcm_layer_plan *out, long long *total_gma);
 
-/* ---- Layers over sequences: a state space block's causal depthwise convolution and selective
- * scan, and its pointwise layers for a few tokens with 4-bit weights.
+/* ---- Layers over sequences: a gated recurrent block's causal depthwise convolution, its recurrence (the
+ * selective scan or the gated delta rule), the normalisation behind it, and its pointwise layers with 4-bit weights.
  *
  * These calls keep no handle: weights are read where they lie, no workspace is needed, nothing
  * is allocated.  Conventions beyond those at the top of this header:
  *  - Every pointer but the descriptor is device memory owned by the caller, aligned to its
- *    element (qw of fcm_w4_matvec: 16 bytes); the calls run on the current device, enqueue on
+ *    element (qw of fcm_w4_matvec, xq and wq of fcm_mx4_matmul: 16 bytes); the calls run on the current device, enqueue on
  *    `stream` and return.  What the host cannot see (seq_start, slot) is bounded by the kernels
  *    as said below: no value in them makes a kernel read or write outside the tensors described
  *    (but for the bytes before a row in the aligned 16-byte piece that it starts in, 14 at most,
@@ -363,7 +363,7 @@ FCM_API fcm_status fcm_fuse_plan(const fcm_layer *layers, int n_layers, int batc
  *    states of the scan, exponentials and activations are float32; each output is rounded once.
  *    NaN goes through every activation (the fused modules' ReLU and ReLU6 make it 0).  silu(v) is -0
  *    for v below -87.34, where its magnitude is 1.03e-36 at most.
- *  - Outputs must not overlap inputs, except that state_out may be state_in itself.
+ *  - Outputs must not overlap inputs, except that state_out may be state_in itself (and y of fcm_group_norm x).
  *  - Kernels are launched with programmatic stream serialization allowed, as fcm_run's are.
  *  - Results do not depend on the launch: the same bits on every run on the same device. */
 
@@ -434,6 +434,72 @@ typedef struct fcm_w4_desc {
 FCM_API fcm_status fcm_w4_matvec(const fcm_w4_desc *desc, const void *x, const void *qw,
                                  const void *qs, const float *s, const float *b, void *y,
                                  void *stream);
+
+/* Gated delta rule: per sequence and head h of key head g = h / (heads / key_heads), with a state S [dk][dv],
+ *     G   = softplus(dt[t,h] + dt_bias[h]) * a[h]           (softplus 0: without softplus)
+ *     B   = 1 / (1 + e^-b[t,h])                             (sigmoid 0: b[t,h])
+ *     q,k = q[t,g,:], k[t,g,:]                              (normalize 1: each over the root of its sum of squares + 1e-6)
+ *     S   = e^G * S;   u = B * (v[t,h,:] - S^T k);   S = S + k u^T
+ *     y[t,h,:] = scale * S^T q
+ * q, k [tokens][key_heads][dk], v, y [tokens][heads][dv], dt, b [tokens][heads], rows ld_* apart; a, dt_bias
+ * [heads] float32 (dt_bias may be NULL: 0).  state_in / state_out [slots][heads][dk][dv] float32 hold S before and
+ * after; state_in NULL starts from zeros, state_out NULL keeps nothing.  dk 1 to 256, dv from 1 on; key_heads divides
+ * heads.  Any dt and a are taken, infinite ones too: e^G is 0 below G = -104, and the state grows where G > 0.
+ * Prompts go through in chunks of rows, whose products meet each other before any sum: a NaN or an infinity among a
+ * head's rows, states or decays may therefore make any row of that head and sequence NaN, earlier ones of the same
+ * chunk too, as may factors e^G whose product over 64 rows leaves a float's range. */
+typedef struct fcm_delta_desc {
+    fcm_seqs seqs;
+    int heads, key_heads, dk, dv, dtype, softplus, sigmoid, normalize;
+    float scale;
+    long long ld_q, ld_k, ld_v, ld_dt, ld_b, ld_y;
+} fcm_delta_desc;
+FCM_API fcm_status fcm_gated_delta(const fcm_delta_desc *desc, const void *q, const void *k, const void *v,
+                                   const void *dt, const float *a, const void *b, const float *dt_bias,
+                                   const float *state_in, void *y, float *state_out, void *stream);
+
+/* Group normalisation with an activation, channels last: x of n samples, each `pixels` rows of c channels, in `groups`
+ * equal groups of neighbouring channels,
+ *     y = act(s[d] * (x - mean) / sqrt(var + eps) + b[d]) * silu(z)
+ * mean and var over a sample's pixels and a group's channels; rms 1: mean is 0 and var the mean of squares.  x, z, y
+ * [n][pixels][c], all n * pixels rows ld_* apart; s, b [c] float32; s, b, z may be NULL (1, 0, no gate).  y may be x
+ * itself (the same pointer and row distance).  pixels 1 normalises a row's groups each by itself: the heads of a
+ * layer over sequences.  eps >= 0; NaN and infinities stay in their sample and group. */
+typedef struct fcm_norm_desc {
+    int n, c, groups, dtype, act, rms;
+    float eps;
+    long long pixels, ld_x, ld_z, ld_y;
+} fcm_norm_desc;
+FCM_API fcm_status fcm_group_norm(const fcm_norm_desc *desc, const void *x, const float *s, const float *b,
+                                  const void *z, void *y, void *stream);
+
+/* Microscaled 4-bit floating point (OCP microscaling format, E2M1 values): rows of `in` values in blocks of 32 that
+ * share a power of two.  q [rows][in/2] bytes, the value of an even place in the low four bits of byte i/2 and the
+ * next one's in the high four: codes 0 to 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, with 8 added for their negatives.
+ * s [rows][in/32] bytes: code e stands for 2^(e-127), 255 for NaN.  in is a multiple of 32.  q and s are contiguous.
+ *
+ * Quantising takes x [m][in] (ld_x apart; FCM_F32, FCM_F16, FCM_BF16): a block's power is 2^(floor(log2(largest
+ * magnitude)) - 2), at least 2^-127, and each value the nearest one after division by it, ties to the even code,
+ * magnitudes above 6 to 6.  A block of zeros has code 0; one that holds an infinity or NaN code 255 and zeros.
+ * Dequantising gives y = value * 2^(e-127) rounded to the storage type, NaN for a block of code 255. */
+typedef struct fcm_mx4_desc {
+    int m, in, dtype;
+    long long ld;          /* of x or y */
+} fcm_mx4_desc;
+FCM_API fcm_status fcm_mx4_quantize(const fcm_mx4_desc *desc, const void *x, void *q, void *s, void *stream);
+FCM_API fcm_status fcm_mx4_dequantize(const fcm_mx4_desc *desc, const void *q, const void *s, void *y, void *stream);
+
+/* Pointwise layer whose rows and weights are both microscaled 4-bit:
+ *     y[t,o] = act(s[o] * sum_i x[t,i] * w[o,i] + b[o])
+ * xq, xs: the m rows; wq, ws: the `out` rows of weights (both as fcm_mx4_quantize leaves them; xq and wq 16-byte
+ * aligned); y [m][out] in FCM_F32, FCM_F16 or FCM_BF16; s, b [out] float32 (NULL: 1, 0).  Sums are float32.  A block
+ * of code 255 makes NaN of its row's sums. */
+typedef struct fcm_mx4_matmul_desc {
+    int m, out, in, dtype, act;
+    long long ld_y;
+} fcm_mx4_matmul_desc;
+FCM_API fcm_status fcm_mx4_matmul(const fcm_mx4_matmul_desc *desc, const void *xq, const void *xs, const void *wq,
+                                  const void *ws, const float *s, const float *b, void *y, void *stream);
 
 #ifdef __cplusplus
 }

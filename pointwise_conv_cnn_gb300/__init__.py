@@ -6,8 +6,8 @@ Argument marshalling only: every step of the computation runs in the CUDA kernel
 library raises instead of falling back.
 
 The functions keep the C names (``fcm_create``, ``fcm_run``, ...).  ``FusedConvModule`` wraps
-a handle for convenience.  ``causal_conv``, ``selective_scan`` and ``w4_matvec`` take tensors for
-the layers over sequences.
+a handle for convenience.  ``causal_conv``, ``selective_scan``, ``gated_delta``, ``group_norm``,
+``w4_matvec`` and the ``mx4_`` functions take tensors for the layers over sequences.
 """
 from __future__ import annotations
 
@@ -28,6 +28,9 @@ __all__ = [
     "DTYPES", "ACTS", "MODES",
     "fcm_causal_conv", "fcm_selective_scan", "fcm_w4_matvec", "FcmSeqs", "FcmCausalConvDesc",
     "FcmScanDesc", "FcmW4Desc", "causal_conv", "selective_scan", "w4_matvec",
+    "fcm_gated_delta", "fcm_group_norm", "fcm_mx4_quantize", "fcm_mx4_dequantize", "fcm_mx4_matmul",
+    "FcmDeltaDesc", "FcmNormDesc", "FcmMx4Desc", "FcmMx4MatmulDesc", "gated_delta", "group_norm",
+    "mx4_quantize", "mx4_dequantize", "mx4_matmul",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,6 +54,7 @@ EXPORTED_SYMBOLS = (
     "fcm_selftest_wait_timeout",
     "fcm_model_pwdw_gma", "fcm_model_pwpw_gma", "fcm_fuse_plan",
     "fcm_causal_conv", "fcm_selective_scan", "fcm_w4_matvec",
+    "fcm_gated_delta", "fcm_group_norm", "fcm_mx4_quantize", "fcm_mx4_dequantize", "fcm_mx4_matmul",
 )
 
 
@@ -125,6 +129,30 @@ class FcmW4Desc(ctypes.Structure):
         (n, ctypes.c_longlong) for n in ("ld_x", "ld_y")]
 
 
+class FcmDeltaDesc(ctypes.Structure):
+    """Mirror of fcm_delta_desc."""
+    _fields_ = [("seqs", FcmSeqs)] + [(n, ctypes.c_int) for n in (
+        "heads", "key_heads", "dk", "dv", "dtype", "softplus", "sigmoid", "normalize")] + [
+        ("scale", ctypes.c_float)] + [(n, ctypes.c_longlong) for n in (
+            "ld_q", "ld_k", "ld_v", "ld_dt", "ld_b", "ld_y")]
+
+
+class FcmNormDesc(ctypes.Structure):
+    """Mirror of fcm_norm_desc."""
+    _fields_ = [(n, ctypes.c_int) for n in ("n", "c", "groups", "dtype", "act", "rms")] + [
+        ("eps", ctypes.c_float)] + [(n, ctypes.c_longlong) for n in ("pixels", "ld_x", "ld_z", "ld_y")]
+
+
+class FcmMx4Desc(ctypes.Structure):
+    """Mirror of fcm_mx4_desc."""
+    _fields_ = [(n, ctypes.c_int) for n in ("m", "in_", "dtype")] + [("ld", ctypes.c_longlong)]
+
+
+class FcmMx4MatmulDesc(ctypes.Structure):
+    """Mirror of fcm_mx4_matmul_desc."""
+    _fields_ = [(n, ctypes.c_int) for n in ("m", "out", "in_", "dtype", "act")] + [("ld_y", ctypes.c_longlong)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -177,7 +205,13 @@ def load_library(path: str | None = None):
         lib.fcm_causal_conv.argtypes = [vp] * 9
         lib.fcm_selective_scan.argtypes = [vp] * 13
         lib.fcm_w4_matvec.argtypes = [vp] * 8
-        for f in ("fcm_causal_conv", "fcm_selective_scan", "fcm_w4_matvec"):
+        lib.fcm_gated_delta.argtypes = [vp] * 12
+        lib.fcm_group_norm.argtypes = [vp] * 7
+        lib.fcm_mx4_quantize.argtypes = [vp] * 5
+        lib.fcm_mx4_dequantize.argtypes = [vp] * 5
+        lib.fcm_mx4_matmul.argtypes = [vp] * 9
+        for f in ("fcm_causal_conv", "fcm_selective_scan", "fcm_w4_matvec", "fcm_gated_delta", "fcm_group_norm",
+                  "fcm_mx4_quantize", "fcm_mx4_dequantize", "fcm_mx4_matmul"):
             getattr(lib, f).restype = i
         del fp
         _lib = lib
@@ -331,6 +365,34 @@ def fcm_w4_matvec(desc: FcmW4Desc, x: int, qw: int, qs: int, s: int, b: int, y: 
     _check(load_library().fcm_w4_matvec(ctypes.addressof(desc), x, qw, qs, s, b, y, stream))
 
 
+def fcm_gated_delta(desc: FcmDeltaDesc, q: int, k: int, v: int, dt: int, a: int, b: int, dt_bias: int,
+                    state_in: int, y: int, state_out: int, stream: int = 0) -> None:
+    """Raw C call; pointers are device addresses (0 or None for the optional ones)."""
+    _check(load_library().fcm_gated_delta(ctypes.addressof(desc), q, k, v, dt, a, b, dt_bias, state_in, y,
+                                          state_out, stream))
+
+
+def fcm_group_norm(desc: FcmNormDesc, x: int, s: int, b: int, z: int, y: int, stream: int = 0) -> None:
+    """Raw C call; pointers are device addresses (0 or None for the optional ones)."""
+    _check(load_library().fcm_group_norm(ctypes.addressof(desc), x, s, b, z, y, stream))
+
+
+def fcm_mx4_quantize(desc: FcmMx4Desc, x: int, q: int, s: int, stream: int = 0) -> None:
+    """Raw C call; pointers are device addresses."""
+    _check(load_library().fcm_mx4_quantize(ctypes.addressof(desc), x, q, s, stream))
+
+
+def fcm_mx4_dequantize(desc: FcmMx4Desc, q: int, s: int, y: int, stream: int = 0) -> None:
+    """Raw C call; pointers are device addresses."""
+    _check(load_library().fcm_mx4_dequantize(ctypes.addressof(desc), q, s, y, stream))
+
+
+def fcm_mx4_matmul(desc: FcmMx4MatmulDesc, xq: int, xs: int, wq: int, ws: int, s: int, b: int, y: int,
+                   stream: int = 0) -> None:
+    """Raw C call; pointers are device addresses (0 or None for the optional ones)."""
+    _check(load_library().fcm_mx4_matmul(ctypes.addressof(desc), xq, xs, wq, ws, s, b, y, stream))
+
+
 def mode_bytes(desc: FcmDesc) -> dict[int, tuple[int, int]]:
     """Bytes each fcm_run mode reads and writes: {mode: (input bytes, output bytes)}."""
     x, m, y = fcm_tensor_bytes(desc)
@@ -460,7 +522,8 @@ def _bind_calls():
         raise FileNotFoundError(f"{os.path.join(_HERE, '_tensor_calls.so')} does not load ({e}): build it "
                                 "with `python -m pointwise_conv_cnn_gb300.build`") from e
     module.bind(FcmError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
-        "fcm_causal_conv", "fcm_selective_scan", "fcm_w4_matvec", "fcm_last_error")))
+        "fcm_causal_conv", "fcm_selective_scan", "fcm_w4_matvec", "fcm_gated_delta", "fcm_group_norm",
+        "fcm_mx4_quantize", "fcm_mx4_dequantize", "fcm_mx4_matmul", "fcm_last_error")))
     _calls = module
     return module
 
@@ -501,3 +564,52 @@ def w4_matvec(x, qw, qs, y, group: int, scale=None, bias=None, act: str = "none"
     even input's value in the low four bits, values 0..15 standing for -8..7; qs: [out,
     ceil(in / group)] in x's dtype; scale, bias: float32 [out]."""
     (_calls or _bind_calls()).w4_matvec(x, qw, qs, y, group, scale, bias, act, stream)
+
+
+def gated_delta(q, k, v, dt, a, b, y, dt_bias=None, softplus: bool = True, sigmoid: bool = True,
+                normalize: bool = True, scale=None, seq_start=None, max_len=None, slot=None, state_in=None,
+                state_out=None, stream=None) -> None:
+    """Gated delta rule over sequences (fcm_gated_delta), enqueued on `stream`.
+
+    q, k: [sequences, length, key heads, dk], or [tokens, key heads, dk] with seq_start; v, y: the same
+    leading shape with [heads, dv] behind it; dt, b: with [heads]; all in q's dtype, rows may be column
+    blocks of wider tensors.  a, dt_bias: float32 [heads].  scale: of the queries (default dk ** -0.5).
+    state_in, state_out: float32 [slots, heads, dk, dv]; seq_start, max_len, slot as for causal_conv."""
+    (_calls or _bind_calls()).gated_delta(
+        q, k, v, dt, a, b, y, dt_bias, softplus, sigmoid, normalize, scale, seq_start, max_len, slot, state_in,
+        state_out, stream)
+
+
+def group_norm(x, y, groups: int, scale=None, bias=None, eps: float = 1e-5, act: str = "none", z=None,
+               rms: bool = False, stream=None) -> None:
+    """Group normalisation, channels last, with an activation and a gate (fcm_group_norm), enqueued on
+    `stream`.
+
+    x, y, z: [samples, .., channels] of one dtype, normalised over all dimensions between and each group's
+    channels; [samples, channels] normalises each row's groups by themselves.  Rows of channels may be
+    column blocks of wider tensors, all the same distance apart; y may be x.  scale, bias: float32
+    [channels]; z: multiplies by silu(z); rms: no mean is taken away."""
+    (_calls or _bind_calls()).group_norm(x, y, groups, scale, bias, eps, act, z, rms, stream)
+
+
+def mx4_quantize(x, q, s, stream=None) -> None:
+    """Rows to microscaled 4-bit floating point (fcm_mx4_quantize), enqueued on `stream`.
+
+    x: [rows, in], rows may be column blocks of a wider tensor; q: uint8 [rows, in / 2], an even place's
+    code in the low four bits; s: uint8 [rows, in / 32], the powers of two that blocks of 32 share."""
+    (_calls or _bind_calls()).mx4_quantize(x, q, s, stream)
+
+
+def mx4_dequantize(q, s, y, stream=None) -> None:
+    """The values of microscaled rows (fcm_mx4_dequantize), enqueued on `stream`; arguments as for
+    mx4_quantize, y: [rows, in]."""
+    (_calls or _bind_calls()).mx4_dequantize(q, s, y, stream)
+
+
+def mx4_matmul(xq, xs, wq, ws, y, scale=None, bias=None, act: str = "none", stream=None) -> None:
+    """Pointwise layer whose rows and weights are both microscaled 4-bit (fcm_mx4_matmul), enqueued on
+    `stream`.
+
+    xq, xs: m rows as mx4_quantize leaves them, wq, ws: `out` rows of weights; y: [m, out] in float32,
+    float16 or bfloat16, rows may be column blocks of a wider tensor; scale, bias: float32 [out]."""
+    (_calls or _bind_calls()).mx4_matmul(xq, xs, wq, ws, y, scale, bias, act, stream)

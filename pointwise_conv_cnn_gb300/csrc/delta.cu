@@ -1,0 +1,237 @@
+// delta.cu -- the gated delta rule: argument checks, the choice of kernel, and the kernel that goes row by
+// row.
+//
+//     S = e^G S;  u = B (v - S^T k);  S = S + k u^T;  y = scale S^T q
+#include "delta.cuh"
+
+namespace fcm {
+namespace seq {
+
+// Row by row.  A block has 32 of a head's value columns, a thread four of them and every 16th row of the
+// state, in registers.  Both products with the state need its value before the row only,
+//     u = B (v - e^G S^T k),   S^T q after it = e^G S^T q + (q.k) u,
+// so that a row costs one sum over the block's threads, through shared memory, and one barrier.  Rows come
+// in batches: their norms, products q.k, decays and steps are made once for all columns by a warp a row.
+// VEC: four columns of the state, v and y are read and written at once.
+template <typename T, int RK, bool VEC>
+__global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const DeltaArgs a) {
+    constexpr int TB = 8, DK = 16 * RK, DV = kDeltaCols;
+    __shared__ float qs[TB][DK], ks[TB][DK], vs[TB][DV];
+    __shared__ float4 row[TB];    // e^G, B, 1 / |k|, scale / |q|
+    __shared__ float prod[TB];    // q.k
+    __shared__ float4 red[2][4][8][2];
+    tc::pdl_wait();
+    tc::pdl_launch_dependents();
+    const int tx = threadIdx.x % 8, ty = threadIdx.x / 8, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int slice = blockIdx.x % a.slices, rest = blockIdx.x / a.slices;
+    const int h = rest % a.heads, q = rest / a.heads, g = h / a.per_key;
+    long long t0;
+    int len;
+    seq_rows(a.q, q, t0, len);
+    const int at = a.state_in || a.state_out ? state_row(a.q, q) : -1;
+    const int d0 = slice * DV, d = d0 + 4 * tx;
+    const size_t cell = ((size_t)max(at, 0) * a.heads + h) * a.dk * a.dv + d;
+    float s[RK][4];
+    const bool from = a.state_in && at >= 0;
+#pragma unroll
+    for (int r = 0; r < RK; r++) {
+        const int i = ty + 16 * r;
+        const float *p = a.state_in + cell + (size_t)i * a.dv;
+        if (VEC) {
+            const float4 v = from && i < a.dk && d < a.dv ? *reinterpret_cast<const float4 *>(p) : make_float4(0, 0, 0, 0);
+            s[r][0] = v.x, s[r][1] = v.y, s[r][2] = v.z, s[r][3] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++) s[r][e] = from && i < a.dk && d + e < a.dv ? p[e] : 0.0f;
+        }
+    }
+    const T *qp = static_cast<const T *>(a.qp) + (size_t)g * a.dk, *kp = static_cast<const T *>(a.kp) + (size_t)g * a.dk;
+    const T *vp = static_cast<const T *>(a.vp) + (size_t)h * a.dv + d0;
+    T *y = static_cast<T *>(a.y) + (size_t)h * a.dv + d;
+    const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+    for (int b0 = 0; b0 < len; b0 += TB) {
+        const int n = min(TB, len - b0);
+        const long long t = t0 + b0;
+        for (int i = threadIdx.x; i < n * DK; i += 128) {
+            const int j = i / DK, e = i % DK;
+            const bool in = e < a.dk;
+            qs[j][e] = in ? Storage<T>::to_f(qp[(t + j) * a.ld_q + e]) : 0.0f;
+            ks[j][e] = in ? Storage<T>::to_f(kp[(t + j) * a.ld_k + e]) : 0.0f;
+        }
+        for (int i = threadIdx.x; i < n * DV; i += 128) {
+            const int j = i / DV, e = i % DV;
+            vs[j][e] = d0 + e < a.dv ? Storage<T>::to_f(vp[(t + j) * a.ld_v + e]) : 0.0f;
+        }
+        __syncthreads();
+        for (int j = warp; j < n; j += 4) {
+            float qq = 0.0f, kk = 0.0f, qk = 0.0f;
+            for (int e = lane; e < DK; e += 32) {
+                const float x = qs[j][e], z = ks[j][e];
+                qq = fmaf(x, x, qq), kk = fmaf(z, z, kk), qk = fmaf(x, z, qk);
+            }
+#pragma unroll
+            for (int m = 16; m; m >>= 1) {
+                qq += __shfl_xor_sync(~0u, qq, m), kk += __shfl_xor_sync(~0u, kk, m), qk += __shfl_xor_sync(~0u, qk, m);
+            }
+            if (lane == 0) {
+                const float dt = Storage<T>::to_f(static_cast<const T *>(a.dt)[(t + j) * a.ld_dt + h]);
+                const float bv = Storage<T>::to_f(static_cast<const T *>(a.b)[(t + j) * a.ld_b + h]);
+                row[j] = make_float4(expf(log_decay(dt + bias, av, a.softplus)), step_of(bv, a.sigmoid),
+                                     a.normalize ? rsqrtf(kk + kDeltaEps) : 1.0f,
+                                     a.normalize ? a.scale * rsqrtf(qq + kDeltaEps) : a.scale);
+                prod[j] = qk;
+            }
+        }
+        __syncthreads();
+        for (int j = 0; j < n; j++) {
+            float pk[4] = {}, pq[4] = {}, kr[RK];
+#pragma unroll
+            for (int r = 0; r < RK; r++) {
+                kr[r] = ks[j][ty + 16 * r];
+                const float qr = qs[j][ty + 16 * r];
+#pragma unroll
+                for (int e = 0; e < 4; e++) pk[e] = fmaf(kr[r], s[r][e], pk[e]), pq[e] = fmaf(qr, s[r][e], pq[e]);
+            }
+#pragma unroll
+            for (int m = 8; m < 32; m <<= 1)
+#pragma unroll
+                for (int e = 0; e < 4; e++) pk[e] += __shfl_xor_sync(~0u, pk[e], m), pq[e] += __shfl_xor_sync(~0u, pq[e], m);
+            if (lane < 8) {
+                red[j & 1][warp][tx][0] = make_float4(pk[0], pk[1], pk[2], pk[3]);
+                red[j & 1][warp][tx][1] = make_float4(pq[0], pq[1], pq[2], pq[3]);
+            }
+            __syncthreads();
+            float4 sk = red[j & 1][0][tx][0], sq = red[j & 1][0][tx][1];
+#pragma unroll
+            for (int w = 1; w < 4; w++) {
+                const float4 x = red[j & 1][w][tx][0], z = red[j & 1][w][tx][1];
+                sk.x += x.x, sk.y += x.y, sk.z += x.z, sk.w += x.w;
+                sq.x += z.x, sq.y += z.y, sq.z += z.z, sq.w += z.w;
+            }
+            const float4 f = row[j], v = *reinterpret_cast<const float4 *>(&vs[j][4 * tx]);
+            const float fk = f.x * f.z;
+            const float u[4] = {f.y * fmaf(-fk, sk.x, v.x), f.y * fmaf(-fk, sk.y, v.y), f.y * fmaf(-fk, sk.z, v.z),
+                                f.y * fmaf(-fk, sk.w, v.w)};
+#pragma unroll
+            for (int r = 0; r < RK; r++) {
+                const float k = f.z * kr[r];
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[r][e] = fmaf(k, u[e], f.x * s[r][e]);
+            }
+            if (ty == 0) {
+                const float qk = f.z * prod[j];
+                const float o[4] = {f.w * fmaf(qk, u[0], f.x * sq.x), f.w * fmaf(qk, u[1], f.x * sq.y),
+                                    f.w * fmaf(qk, u[2], f.x * sq.z), f.w * fmaf(qk, u[3], f.x * sq.w)};
+                T *to = y + (t + j) * a.ld_y;
+                if (VEC) {
+                    if (d < a.dv) reinterpret_cast<Vec<T, 4> *>(to)->put(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (d + e < a.dv) to[e] = Storage<T>::from_f(o[e]);
+                }
+            }
+        }
+        __syncthreads();   // the next batch overwrites this one's rows
+    }
+    if (a.state_out && at >= 0) {
+#pragma unroll
+        for (int r = 0; r < RK; r++) {
+            const int i = ty + 16 * r;
+            float *p = a.state_out + cell + (size_t)i * a.dv;
+            if (i >= a.dk) continue;
+            if (VEC) {
+                if (d < a.dv) *reinterpret_cast<float4 *>(p) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (d + e < a.dv) p[e] = s[r][e];
+            }
+        }
+    }
+}
+
+template <typename T> static cudaError_t run_delta(const DeltaArgs &a, int sms, cudaStream_t st) {
+    const size_t v = 4 * sizeof(T);
+    auto by = [](const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    const bool vec = a.dv % 4 == 0 && by(a.state_in, 16) && by(a.state_out, 16) && by(a.y, v) && a.ld_y % 4 == 0;
+    const dim3 grid((unsigned)((long long)a.q.n_seq * a.heads * a.slices));
+#define ROWS(rk) launch(vec ? delta_row_kernel<T, rk, true> : delta_row_kernel<T, rk, false>, grid, 128, 0, st, a)
+    return a.dk <= 64 ? ROWS(4) : a.dk <= 128 ? ROWS(8) : ROWS(16);
+#undef ROWS
+}
+
+}  // namespace seq
+}  // namespace fcm
+
+using namespace fcm;
+
+extern "C" fcm_status fcm_gated_delta(const fcm_delta_desc *desc, const void *q, const void *k, const void *v,
+                                      const void *dt, const float *a, const void *b, const float *dt_bias,
+                                      const float *state_in, void *y, float *state_out, void *stream) {
+    FcmNvtxRange nvtx("fcm_gated_delta");
+    if (!desc) return fcm_fail(FCM_ERR_INVALID_ARG, "desc is NULL");
+    fcm_delta_desc d = *desc;
+    if (d.heads < 1 || d.key_heads < 1 || d.dk < 1 || d.dv < 1)
+        return fcm_fail(FCM_ERR_INVALID_ARG, "heads %d, key_heads %d, dk %d, dv %d", d.heads, d.key_heads, d.dk, d.dv);
+    if (d.heads % d.key_heads)
+        return fcm_fail(FCM_ERR_INVALID_ARG, "%d key heads do not divide %d heads", d.key_heads, d.heads);
+    if (d.dk > seq::kMaxDeltaKeys) return fcm_fail(FCM_ERR_UNSUPPORTED, "dk %d above %d", d.dk, seq::kMaxDeltaKeys);
+    if (d.dtype < FCM_F32 || d.dtype > FCM_BF16)
+        return fcm_fail(FCM_ERR_UNSUPPORTED, "dtype %d: f32, f16 and bf16 are supported", d.dtype);
+    for (const int flag : {d.softplus, d.sigmoid, d.normalize})
+        if (flag != 0 && flag != 1)
+            return fcm_fail(FCM_ERR_INVALID_ARG, "softplus %d, sigmoid %d, normalize %d: 0 or 1", d.softplus, d.sigmoid,
+                            d.normalize);
+    const long long ck = (long long)d.key_heads * d.dk, cv = (long long)d.heads * d.dv;
+    if (cv * d.dk > 0x7FFFFFFFLL) return fcm_fail(FCM_ERR_UNSUPPORTED, "heads * dk * dv above 2^31 - 1");
+    seq::DeltaArgs g = {};
+    fcm_status st;
+    if ((st = seq::check_seqs(d.seqs, state_in || state_out, &g.q)) != FCM_OK ||
+        (st = seq::check_ld(&d.ld_q, ck, "ld_q")) != FCM_OK || (st = seq::check_ld(&d.ld_k, ck, "ld_k")) != FCM_OK ||
+        (st = seq::check_ld(&d.ld_v, cv, "ld_v")) != FCM_OK ||
+        (st = seq::check_ld(&d.ld_dt, d.heads, "ld_dt")) != FCM_OK ||
+        (st = seq::check_ld(&d.ld_b, d.heads, "ld_b")) != FCM_OK || (st = seq::check_ld(&d.ld_y, cv, "ld_y")) != FCM_OK)
+        return st;
+    if (g.q.n_seq == 0) return FCM_OK;
+    const size_t e = (size_t)fcm_dtype_bytes(d.dtype);
+    const long long rows = g.q.tokens;   // without rows the activations may be NULL
+    if ((rows && ((st = seq::check_dev_ptr(q, e, "q")) != FCM_OK || (st = seq::check_dev_ptr(k, e, "k")) != FCM_OK ||
+                  (st = seq::check_dev_ptr(v, e, "v")) != FCM_OK || (st = seq::check_dev_ptr(dt, e, "dt")) != FCM_OK ||
+                  (st = seq::check_dev_ptr(b, e, "b")) != FCM_OK || (st = seq::check_dev_ptr(y, e, "y")) != FCM_OK)) ||
+        (st = seq::check_dev_ptr(a, 4, "a")) != FCM_OK ||
+        (dt_bias && (st = seq::check_dev_ptr(dt_bias, 4, "dt_bias")) != FCM_OK) ||
+        (state_in && (st = seq::check_dev_ptr(state_in, 4, "state_in")) != FCM_OK) ||
+        (state_out && (st = seq::check_dev_ptr(state_out, 4, "state_out")) != FCM_OK))
+        return st;
+    const struct {
+        const void *p;
+        long long ld, cols;
+        const char *name;
+    } ins[] = {{q, d.ld_q, ck, "q"}, {k, d.ld_k, ck, "k"}, {v, d.ld_v, cv, "v"}, {dt, d.ld_dt, d.heads, "dt"},
+               {b, d.ld_b, d.heads, "b"}};
+    for (const auto &in : ins)
+        if (seq::rows_overlap(in.p, in.ld, in.cols, y, d.ld_y, cv, rows, e))
+            return fcm_fail(FCM_ERR_INVALID_ARG, "%s and y overlap", in.name);
+    const long long cells = cv * d.dk;
+    if (state_in != state_out && seq::rows_overlap(state_in, cells, cells, state_out, cells, cells, g.q.slots, 4))
+        return fcm_fail(FCM_ERR_INVALID_ARG, "state_in and state_out overlap without being the same");
+    g.slices = (d.dv + seq::kDeltaCols - 1) / seq::kDeltaCols;
+    if ((long long)g.q.n_seq * d.heads * g.slices > 0x7FFFFFFFLL)
+        return fcm_fail(FCM_ERR_UNSUPPORTED, "%d sequences of %d heads of %d columns: above 2^31 - 1 blocks", g.q.n_seq,
+                        d.heads, d.dv);
+    int sms;
+    if ((st = seq::current_device(&sms)) != FCM_OK) return st;
+
+    g.qp = q, g.kp = k, g.vp = v, g.dt = dt, g.b = b, g.a = a, g.dt_bias = dt_bias, g.state_in = state_in;
+    g.y = y, g.state_out = state_out;
+    g.ld_q = d.ld_q, g.ld_k = d.ld_k, g.ld_v = d.ld_v, g.ld_dt = d.ld_dt, g.ld_b = d.ld_b, g.ld_y = d.ld_y;
+    g.heads = d.heads, g.per_key = d.heads / d.key_heads, g.dk = d.dk, g.dv = d.dv;
+    g.softplus = d.softplus, g.sigmoid = d.sigmoid, g.normalize = d.normalize, g.scale = d.scale;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t ce = d.dtype == FCM_F32   ? seq::run_delta<float>(g, sms, cs)
+                           : d.dtype == FCM_F16 ? seq::run_delta<__half>(g, sms, cs)
+                                                : seq::run_delta<__nv_bfloat16>(g, sms, cs);
+    if (ce != cudaSuccess) return fcm_fail(FCM_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(ce));
+    return FCM_OK;
+}

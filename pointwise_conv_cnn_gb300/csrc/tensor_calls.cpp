@@ -1,5 +1,5 @@
 // tensor_calls.cpp -- argument marshalling from torch tensors to the C ABI's layers over sequences
-// (include/fcm.h), for the package's causal_conv, selective_scan and w4_matvec.  A single token's
+// (include/fcm.h), for the package's functions that take tensors (causal_conv and those below it).  A single token's
 // kernel takes two or three microseconds, checking a call's dozen tensors attribute by attribute
 // in Python ten; here it is less than one.  Nothing is computed, allocated or kept.
 #define PY_SSIZE_T_CLEAN
@@ -8,6 +8,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstring>
 #include <sstream>
 #include <string>
@@ -20,6 +21,11 @@ PyObject *g_error = nullptr;   // FcmError
 decltype(&fcm_causal_conv) g_conv = nullptr;
 decltype(&fcm_selective_scan) g_scan = nullptr;
 decltype(&fcm_w4_matvec) g_w4 = nullptr;
+decltype(&fcm_gated_delta) g_delta = nullptr;
+decltype(&fcm_group_norm) g_norm = nullptr;
+decltype(&fcm_mx4_quantize) g_mx4_quantize = nullptr;
+decltype(&fcm_mx4_dequantize) g_mx4_dequantize = nullptr;
+decltype(&fcm_mx4_matmul) g_mx4_matmul = nullptr;
 decltype(&fcm_last_error) g_last_error = nullptr;
 
 struct Refusal {
@@ -59,13 +65,13 @@ const at::Tensor *optional_tensor(PyObject *o, const char *what) {
     return o == Py_None ? nullptr : &tensor(o, what);
 }
 
-int dtype_code(const at::Tensor &x) {
+int dtype_code(const at::Tensor &x, const char *what = "x") {
     switch (x.scalar_type()) {
     case at::kFloat: return FCM_F32;
     case at::kHalf: return FCM_F16;
     case at::kBFloat16: return FCM_BF16;
     default:
-        refuse(FCM_ERR_UNSUPPORTED, "x is torch.",
+        refuse(FCM_ERR_UNSUPPORTED, what, " is torch.",
                x.scalar_type() == at::kDouble ? "float64" : c10::toString(x.scalar_type()),
                ": float32, float16, bfloat16 are supported");
     }
@@ -133,17 +139,36 @@ int act_code(PyObject *o) {
     refuse(FCM_ERR_INVALID_ARG, "activation ", s ? s : "must be a name", ": none, relu, relu6 or silu");
 }
 
-// The sequences of x [sequences, length, c], or of x [tokens, c] with seq_start.
+bool truth(PyObject *o, const char *what) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        refuse(FCM_ERR_INVALID_ARG, what, " must be true or false");
+    }
+    return v != 0;
+}
+
+float number(PyObject *o, const char *what) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(FCM_ERR_INVALID_ARG, what, " must be a number");
+    }
+    return (float)v;
+}
+
+// The sequences of x [sequences, length, row], or of x [tokens, row] with seq_start, whose rows have `row`
+// dimensions.
 fcm_seqs sequences(const at::Tensor &x, const at::Tensor *seq_start, PyObject *max_len, const at::Tensor *slot,
-                   const at::Tensor *state) {
+                   const at::Tensor *state, int row = 1, const char *what = "x", const char *dims = "channels") {
     fcm_seqs s = {};
     if (!seq_start) {
-        if (x.dim() != 3)
-            refuse(FCM_ERR_INVALID_ARG, "x must be [sequences, length, channels], or [tokens, channels] with seq_start");
+        if (x.dim() != 2 + row)
+            refuse(FCM_ERR_INVALID_ARG, what, " must be [sequences, length, ", dims, "], or [tokens, ", dims, "] with seq_start");
         s.n_seq = as_int(x.size(0), "sequences"), s.max_len = as_int(x.size(1), "length");
         s.tokens = (long long)s.n_seq * s.max_len;
     } else {
-        if (x.dim() != 2) refuse(FCM_ERR_INVALID_ARG, "x must be [tokens, channels] with seq_start");
+        if (x.dim() != 1 + row) refuse(FCM_ERR_INVALID_ARG, what, " must be [tokens, ", dims, "] with seq_start");
         if (seq_start->dim() != 1 || seq_start->size(0) < 1)
             refuse(FCM_ERR_INVALID_ARG, "seq_start must have one element more than there are sequences");
         s.tokens = x.size(0);
@@ -166,9 +191,9 @@ fcm_seqs sequences(const at::Tensor &x, const at::Tensor *seq_start, PyObject *m
 
 // The stream given (its handle, or an object that has it as cuda_stream), or the current one; x must
 // lie on the current device.
-void *stream_of(const at::Tensor &x, PyObject *stream) {
+void *stream_of(const at::Tensor &x, PyObject *stream, const char *what = "x") {
     if (!x.is_cuda() || x.get_device() != c10::cuda::current_device())
-        refuse(FCM_ERR_INVALID_ARG, "x must be a CUDA tensor on the current device");
+        refuse(FCM_ERR_INVALID_ARG, what, " must be a CUDA tensor on the current device");
     if (stream == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
     PyObject *handle = PyObject_GetAttrString(stream, "cuda_stream");
     if (!handle) {
@@ -248,12 +273,7 @@ PyObject *selective_scan(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         const int64_t ch = x.sizes().back(), n = av.size(1), slots = d.seqs.slots;
         const auto lead = x.sizes().slice(0, x.dim() - 1);
         d.c = as_int(ch, "channels"), d.n_state = as_int(n, "states");
-        const int softplus = PyObject_IsTrue(a[9]);
-        if (softplus < 0) {
-            PyErr_Clear();
-            refuse(FCM_ERR_INVALID_ARG, "softplus must be true or false");
-        }
-        d.softplus = softplus;
+        d.softplus = truth(a[9], "softplus");
         d.ld_x = rows(x, x, lead, {ch}, "x"), d.ld_dt = rows(dt, x, lead, {ch}, "dt");
         if (b.dim() == x.dim() + 1) {
             const int64_t g = b.size(-2);
@@ -300,11 +320,142 @@ PyObject *w4_matvec(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// q, k, v, dt, a, b, y, dt_bias, softplus, sigmoid, normalize, scale, seq_start, max_len, slot, state_in, state_out, stream
+PyObject *gated_delta(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 18, [&]() -> int {
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &dt = tensor(a[3], "dt");
+        const at::Tensor &av = tensor(a[4], "a"), &b = tensor(a[5], "b"), &y = tensor(a[6], "y");
+        const at::Tensor *in = optional_tensor(a[15], "state_in"), *out = optional_tensor(a[16], "state_out");
+        fcm_delta_desc d = {};
+        d.dtype = dtype_code(q, "q");
+        d.seqs = sequences(q, optional_tensor(a[12], "seq_start"), a[13], optional_tensor(a[14], "slot"), in ? in : out, 2,
+                           "q", "key heads, dk");
+        if (v.dim() != q.dim()) refuse(FCM_ERR_INVALID_ARG, "v must be shaped as q is, with [heads, dv] at its end");
+        const int64_t hk = q.size(-2), dk = q.size(-1), h = v.size(-2), dv = v.size(-1), slots = d.seqs.slots;
+        const auto lead = q.sizes().slice(0, q.dim() - 2);
+        d.key_heads = as_int(hk, "key heads"), d.dk = as_int(dk, "dk"), d.heads = as_int(h, "heads"), d.dv = as_int(dv, "dv");
+        d.softplus = truth(a[8], "softplus"), d.sigmoid = truth(a[9], "sigmoid"), d.normalize = truth(a[10], "normalize");
+        d.scale = a[11] == Py_None ? (float)(1.0 / std::sqrt((double)(dk ? dk : 1))) : number(a[11], "scale");
+        d.ld_q = rows(q, q, lead, {hk, dk}, "q"), d.ld_k = rows(k, q, lead, {hk, dk}, "k");
+        d.ld_v = rows(v, q, lead, {h, dv}, "v"), d.ld_dt = rows(dt, q, lead, {h}, "dt");
+        d.ld_b = rows(b, q, lead, {h}, "b"), d.ld_y = rows(y, q, lead, {h, dv}, "y");
+        const float *ap = plain<const float>(&av, q, at::kFloat, {h}, "a");
+        const float *bias = plain<const float>(optional_tensor(a[7], "dt_bias"), q, at::kFloat, {h}, "dt_bias");
+        const float *sin = plain<const float>(in, q, at::kFloat, {slots, h, dk, dv}, "state_in");
+        float *sout = plain<float>(out, q, at::kFloat, {slots, h, dk, dv}, "state_out");
+        return g_delta(&d, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), ap, b.data_ptr(), bias, sin, y.data_ptr(),
+                       sout, stream_of(q, a[17], "q"));
+    });
+}
+
+// The distance of all rows of activations [sample, .., channel] behind one another, as if they were [rows, c]:
+// dimensions of one element say nothing, the others have to continue each other.
+int64_t pixel_rows(const at::Tensor &t, const at::Tensor &x, const char *what) {
+    if (t.scalar_type() != x.scalar_type() || t.device() != x.device() || t.sizes() != x.sizes())
+        refuse(FCM_ERR_INVALID_ARG, what, " must be a ", c10::toString(x.scalar_type()), " tensor of shape ",
+               shape_of(x.sizes()), " on x's device, not ", described(t));
+    const auto size = t.sizes(), stride = t.strides();
+    const int64_t c = size.back();
+    if (t.numel() == 0) return c;
+    if (c > 1 && stride.back() != 1)
+        refuse(FCM_ERR_INVALID_ARG, what, ": a row's elements must lie together, strides ", shape_of(stride));
+    int64_t ld = c, next = 0;   // next: the stride that the dimension before has to have; 0: any
+    for (size_t i = size.size() - 1; i-- > 0;) {
+        if (size[i] == 1) continue;
+        if (!next) ld = stride[i];
+        else if (stride[i] != next)
+            refuse(FCM_ERR_INVALID_ARG, what, ": rows must all be the same distance apart, strides ", shape_of(stride));
+        next = stride[i] * size[i];
+    }
+    if (ld < c) refuse(FCM_ERR_INVALID_ARG, what, ": rows overlap, strides ", shape_of(stride));
+    return ld;
+}
+
+// x, y, groups, scale, bias, eps, act, z, rms, stream
+PyObject *group_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> int {
+        const at::Tensor &x = tensor(a[0], "x"), &y = tensor(a[1], "y");
+        const at::Tensor *z = optional_tensor(a[7], "z");
+        fcm_norm_desc d = {};
+        d.dtype = dtype_code(x);
+        if (x.dim() < 2) refuse(FCM_ERR_INVALID_ARG, "x must be [samples, channels] or [samples, .., channels]");
+        const int64_t c = x.sizes().back();
+        d.n = as_int(x.size(0), "samples"), d.c = as_int(c, "channels"), d.pixels = 1;
+        for (int64_t i = 1; i + 1 < x.dim(); i++) d.pixels *= x.size(i);
+        const long groups = PyLong_AsLong(a[2]);
+        if (groups == -1 && PyErr_Occurred()) {
+            PyErr_Clear();
+            refuse(FCM_ERR_INVALID_ARG, "groups must be a whole number");
+        }
+        if (groups < 1 || groups > c || c % groups)
+            refuse(FCM_ERR_INVALID_ARG, groups, " groups do not divide ", c, " channels");
+        d.groups = (int)groups, d.act = act_code(a[6]), d.rms = truth(a[8], "rms"), d.eps = number(a[5], "eps");
+        d.ld_x = pixel_rows(x, x, "x"), d.ld_y = pixel_rows(y, x, "y");
+        if (z) d.ld_z = pixel_rows(*z, x, "z");
+        const float *s = plain<const float>(optional_tensor(a[3], "scale"), x, at::kFloat, {c}, "scale");
+        const float *b = plain<const float>(optional_tensor(a[4], "bias"), x, at::kFloat, {c}, "bias");
+        return g_norm(&d, x.data_ptr(), s, b, z ? z->data_ptr() : nullptr, y.data_ptr(), stream_of(x, a[9]));
+    });
+}
+
+// x (or y), q, s of microscaled rows
+fcm_mx4_desc mx4_rows(const at::Tensor &x, const at::Tensor &q, const at::Tensor &s, const char *what) {
+    fcm_mx4_desc d = {};
+    d.dtype = dtype_code(x, what);
+    if (x.dim() != 2) refuse(FCM_ERR_INVALID_ARG, what, " must be [rows, in]");
+    const int64_t m = x.size(0), k = x.size(1);
+    if (k % 32) refuse(FCM_ERR_UNSUPPORTED, "in ", k, " is not a multiple of 32");
+    d.m = as_int(m, "rows"), d.in = as_int(k, "in");
+    d.ld = rows(x, x, x.sizes().slice(0, 1), {k}, what);
+    plain(&q, x, at::kByte, {m, k / 2}, "q"), plain(&s, x, at::kByte, {m, k / 32}, "s");
+    return d;
+}
+
+// x, q, s, stream
+PyObject *mx4_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 4, [&]() -> int {
+        const at::Tensor &x = tensor(a[0], "x"), &q = tensor(a[1], "q"), &s = tensor(a[2], "s");
+        const fcm_mx4_desc d = mx4_rows(x, q, s, "x");
+        return g_mx4_quantize(&d, x.data_ptr(), q.data_ptr(), s.data_ptr(), stream_of(x, a[3]));
+    });
+}
+
+// q, s, y, stream
+PyObject *mx4_dequantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 4, [&]() -> int {
+        const at::Tensor &q = tensor(a[0], "q"), &s = tensor(a[1], "s"), &y = tensor(a[2], "y");
+        const fcm_mx4_desc d = mx4_rows(y, q, s, "y");
+        return g_mx4_dequantize(&d, q.data_ptr(), s.data_ptr(), y.data_ptr(), stream_of(y, a[3], "y"));
+    });
+}
+
+// xq, xs, wq, ws, y, scale, bias, act, stream
+PyObject *mx4_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> int {
+        const at::Tensor &xq = tensor(a[0], "xq"), &xs = tensor(a[1], "xs"), &wq = tensor(a[2], "wq"), &ws = tensor(a[3], "ws");
+        const at::Tensor &y = tensor(a[4], "y");
+        fcm_mx4_matmul_desc d = {};
+        d.dtype = dtype_code(y, "y");
+        if (xq.dim() != 2 || wq.dim() != 2) refuse(FCM_ERR_INVALID_ARG, "xq must be [m, in / 2] and wq [out, in / 2]");
+        const int64_t m = xq.size(0), o = wq.size(0), k = 2 * xq.size(1);
+        if (k % 32) refuse(FCM_ERR_UNSUPPORTED, "in ", k, " is not a multiple of 32");
+        d.m = as_int(m, "m"), d.out = as_int(o, "out"), d.in = as_int(k, "in"), d.act = act_code(a[7]);
+        const int64_t lead[1] = {m};
+        d.ld_y = rows(y, y, lead, {o}, "y");
+        const void *xp = plain(&xq, y, at::kByte, {m, k / 2}, "xq"), *xsp = plain(&xs, y, at::kByte, {m, k / 32}, "xs");
+        const void *wp = plain(&wq, y, at::kByte, {o, k / 2}, "wq"), *wsp = plain(&ws, y, at::kByte, {o, k / 32}, "ws");
+        const float *s = plain<const float>(optional_tensor(a[5], "scale"), y, at::kFloat, {o}, "scale");
+        const float *b = plain<const float>(optional_tensor(a[6], "bias"), y, at::kFloat, {o}, "bias");
+        return g_mx4_matmul(&d, xp, xsp, wp, wsp, s, b, y.data_ptr(), stream_of(y, a[8], "y"));
+    });
+}
+
 // FcmError and the addresses of the library's entry points, once, before any call.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    void *p[4] = {};
-    if (n != 5) return PyErr_Format(PyExc_TypeError, "bind takes the error class and four addresses");
-    for (int i = 0; i < 4; i++) {
+    constexpr int kCalls = 9;
+    void *p[kCalls] = {};
+    if (n != kCalls + 1) return PyErr_Format(PyExc_TypeError, "bind takes the error class and %d addresses", kCalls);
+    for (int i = 0; i < kCalls; i++) {
         p[i] = PyLong_AsVoidPtr(a[i + 1]);
         if (!p[i]) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "a NULL address");
     }
@@ -314,12 +465,19 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g_conv = reinterpret_cast<decltype(g_conv)>(p[0]);
     g_scan = reinterpret_cast<decltype(g_scan)>(p[1]);
     g_w4 = reinterpret_cast<decltype(g_w4)>(p[2]);
-    g_last_error = reinterpret_cast<decltype(g_last_error)>(p[3]);
+    g_delta = reinterpret_cast<decltype(g_delta)>(p[3]);
+    g_norm = reinterpret_cast<decltype(g_norm)>(p[4]);
+    g_mx4_quantize = reinterpret_cast<decltype(g_mx4_quantize)>(p[5]);
+    g_mx4_dequantize = reinterpret_cast<decltype(g_mx4_dequantize)>(p[6]);
+    g_mx4_matmul = reinterpret_cast<decltype(g_mx4_matmul)>(p[7]);
+    g_last_error = reinterpret_cast<decltype(g_last_error)>(p[8]);
     Py_RETURN_NONE;
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(bind), FAST(causal_conv), FAST(selective_scan), FAST(w4_matvec), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST(bind), FAST(causal_conv), FAST(selective_scan), FAST(w4_matvec), FAST(gated_delta),
+                         FAST(group_norm), FAST(mx4_quantize), FAST(mx4_dequantize), FAST(mx4_matmul),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
