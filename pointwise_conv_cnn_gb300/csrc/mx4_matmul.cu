@@ -1,6 +1,8 @@
 // mx4_matmul.cu -- pointwise layer whose rows and weights are both microscaled 4-bit.
 //
 //     y[t,o] = act(s[o] * sum_i x[t,i] * w[o,i] + b[o])
+#include <atomic>
+
 #include "mx4.cuh"
 #include "seq_common.cuh"
 #include "tc_common.cuh"
@@ -9,51 +11,314 @@ namespace fcm {
 namespace seq {
 
 struct Mx4MatmulArgs {
-    const uint8_t *xq, *xs, *wq, *ws;
+    CUtensorMap wmap, xmap;   // rows of bytes: weights, tokens
+    const uint8_t *ws, *xs;
     const float *s, *b;
     void *y;
     long long ld_y;
-    int m, out, in, act;
+    int m, out, groups, act, dtype;
+    int chunks;        // of 512 inputs
+    int split;         // blocks of a cluster, which share the inputs
+    int wvec, xvec;    // rows of scales may be read 16 bytes at a time
 };
 
-// 64 rows by 64 outputs a block, a block of 32 inputs at a time: both factors widened in shared memory, four by
-// four sums a thread.
-template <typename T> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const Mx4MatmulArgs a) {
-    __shared__ float xt[32][65], wt[32][65];
+// Descriptor of a product of microscaled 4-bit factors (E2M1, scales powers of two): 128 x n x 64, both factors with
+// their inputs side by side; `sf` selects bytes sf, sf + 1 of each scale word.
+__host__ __device__ constexpr uint32_t idesc_mx4(int n, uint32_t sf) {
+    return sf << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | 1u << 23 | 1u << 27 | sf << 29;
+}
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// 32 rows of 16 bytes, side by side in shared memory, to four columns of each of the tensor memory's quarters.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+    const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// A block: 128 outputs of NT tokens.  Rows of the product are outputs, so that a warp's stores of a token are side by
+// side.  Inputs go in stages of 256, 128 bytes a row.
+template <int NT> struct Mx4Shape {
+    static constexpr int ST = NT == 128 ? 3 : 4;             // stages; two blocks an SM up to 128 tokens
+    static constexpr int NB = (NT + 127) / 128;              // blocks of 128 tokens
+    static constexpr int A = 128 * 128, B = NT * 128;        // bytes of a stage
+    static constexpr int SF = 1024 * (1 + NB);               // of its scales: two words of four for each row
+    static constexpr int SMEM = ST * (A + B + SF) + 1024 /* alignment */ + 256 /* barriers */;
+    static constexpr int ACC = NT < 32 ? 32 : NT;
+    static constexpr int SFC = 8 * (1 + NB);                 // columns of a stage's scales
+    static constexpr int COLS = ACC + ST * SFC <= 128 ? 128 : ACC + ST * SFC <= 256 ? 256 : 512;
+    static_assert(ST * (A + B) >= 128 * NT * 4, "the sums of a split product take the stages' place");
+};
+
+// The 16 scale codes of `rows` rows for one chunk of 512 inputs, by a warp: on their way to shared memory as 4 blocks
+// (of 128 inputs) of 32 x 16 bytes, row r's word at (r % 32) * 16 + (r / 32) * 4.
+// Where rows of codes start at 16 bytes a lane has rows lane, lane + 32, .. whole, and stores 16 bytes a block.
+// Else four lanes have a row, a word each, taken from the two aligned words that it lies in.
+struct ScaleChunk {
+    uint32_t w[16];
+    __device__ __forceinline__ void load(const uint8_t *s, int vec, int row0, int rows, int last_row, int groups, int g0, int lane) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = min(row0 + i * 32 + lane, last_row);
+                const uint4 v = i * 32 < rows && g0 < groups
+                                    ? *reinterpret_cast<const uint4 *>(s + (size_t)r * groups + g0) : make_uint4(0, 0, 0, 0);
+                w[i] = v.x, w[4 + i] = v.y, w[8 + i] = v.z, w[12 + i] = v.w;
+            }
+        } else {
+            const int g = g0 + lane % 4 * 4, have = min(groups - g, 4);   // codes of this word
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const int r = min(row0 + i * 8 + lane / 4, last_row);
+                const uintptr_t at = reinterpret_cast<uintptr_t>(s + (size_t)r * groups + g);
+                const uint32_t off = at & 3;
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(at - off);
+                uint32_t lo = 0, hi = 0;
+                if (i * 8 < rows && have > 0) lo = p[0];
+                if (i * 8 < rows && (int)off + have > 4) hi = p[1];
+                w[i] = __funnelshift_r(lo, hi, off * 8);
+            }
+            const uint32_t keep = have >= 4 ? ~0u : have <= 0 ? 0u : (1u << (8 * have)) - 1;
+#pragma unroll
+            for (int i = 0; i < 16; i++) w[i] &= keep;   // codes past the last: any number, their values are 0
+        }
+    }
+    // the blocks 2 * half and 2 * half + 1, one stage's
+    __device__ __forceinline__ void store(uint32_t to, int vec, int half, int lane) const {
+        if (vec) {
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                if (half == 0) tc::sts128(to + k * 512 + lane * 16, w[k * 4], w[k * 4 + 1], w[k * 4 + 2], w[k * 4 + 3]);
+                else tc::sts128(to + k * 512 + lane * 16, w[8 + k * 4], w[9 + k * 4], w[10 + k * 4], w[11 + k * 4]);
+            }
+        } else if ((lane & 2) == 2 * half) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const int r = i * 8 + lane / 4;
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (lane & 1) * 512 + r % 32 * 16 + r / 32 * 4), "r"(w[i]) : "memory");
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void mx4_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Warp 0 asks for the factors (TMA), warp 1 multiplies, warps 4 to 6 bring the scales to shared memory, from where warp
+// 1 has them copied to tensor memory ahead of its products, and warps 4 to 7 finish.  A bounded wait that runs out ends
+// the block with NaN for its outputs.
+template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const __grid_constant__ Mx4MatmulArgs a) {
+    using S = Mx4Shape<NT>;
+    extern __shared__ unsigned char raw[];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ unsigned error;
+    const uint32_t base = (tc::smem_u32(raw) + 1023) & ~1023u;
+    const uint32_t at_a = base, at_b = at_a + S::ST * S::A, at_sf = at_b + S::ST * S::B, bars = at_sf + S::ST * S::SF;
+    const uint32_t full = bars, sf_full = bars + 8 * S::ST, empty = bars + 16 * S::ST, done = bars + 24 * S::ST;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const unsigned tile = blockIdx.x / a.split, rank = blockIdx.x % a.split, tiles_m = (unsigned)(a.m + NT - 1) / NT;
+    const int m0 = (int)(tile % tiles_m) * NT, o0 = (int)(tile / tiles_m) * 128;
+    const int c0 = (int)((long long)a.chunks * rank / a.split), c1 = (int)((long long)a.chunks * (rank + 1) / a.split);
+    const int stages = min(2 * c1, (a.groups + 7) / 8) - 2 * c0;   // of 8 codes
+    volatile int *abort = &abort_flag;
+    if (threadIdx.x == 0) {
+        abort_flag = 0, error = 0;
+        for (int i = 0; i < S::ST; i++) {
+            tc::mbar_init(full + 8 * i, 1);
+            tc::mbar_init(sf_full + 8 * i, 1 + S::NB);
+            tc::mbar_init(empty + 8 * i, 1);
+        }
+        tc::mbar_init(done, 1);
+        tc::fence_barrier_init();
+        tc::tma_prefetch_desc(&a.wmap);
+        tc::tma_prefetch_desc(&a.xmap);
+    }
+    if (warp == 2) tc::tmem_alloc(tc::smem_u32(&tmem_slot), S::COLS);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
     tc::pdl_wait();
     tc::pdl_launch_dependents();
-    const int m0 = blockIdx.y * 64, o0 = blockIdx.x * 64;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, r = threadIdx.x / 4, part = threadIdx.x % 4;
-    const int half = a.in / 2, groups = a.in / 32;
-    float sum[4][4] = {};
-    for (int g = 0; g < groups; g++) {
-        const int xr = min(m0 + r, a.m - 1), wr = min(o0 + r, a.out - 1);
-        const uint32_t x = reinterpret_cast<const uint32_t *>(a.xq + (size_t)xr * half)[g * 4 + part];
-        const uint32_t w = reinterpret_cast<const uint32_t *>(a.wq + (size_t)wr * half)[g * 4 + part];
-        const float xb = power_of(a.xs[(size_t)xr * groups + g]), wb = power_of(a.ws[(size_t)wr * groups + g]);
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            xt[part * 8 + i][r] = e2m1_value(x >> (4 * i)) * xb;
-            wt[part * 8 + i][r] = e2m1_value(w >> (4 * i)) * wb;
+    auto wait = [&](uint32_t bar, uint32_t parity) { return tc::mbar_wait(bar, parity, abort, &error, tc::kWaitLimitNs); };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (; it < stages; it++) {
+                const int s = it % S::ST;
+                if (it >= S::ST && !wait(empty + 8 * s, (it / S::ST - 1) & 1)) break;
+                tc::mbar_arrive_expect_tx(full + 8 * s, S::A + S::B);
+                const int x = (2 * c0 + it) * 128;
+                tc::tma_load_2d(at_a + s * S::A, &a.wmap, full + 8 * s, x, o0);
+                tc::tma_load_2d(at_b + s * S::B, &a.xmap, full + 8 * s, x, m0);
+            }
+            // what is on its way has arrived before the block ends
+            for (int i = max(0, it - S::ST); i < it; i++)
+                for (int n = 0; n < (1 << 20) && !tc::mbar_try_wait(full + 8 * (i % S::ST), (i / S::ST) & 1); n++) {}
         }
-        __syncthreads();
-#pragma unroll 8
-        for (int i = 0; i < 32; i++)
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t sft = tmem + S::ACC;
+            for (int it = 0; it < stages; it++) {
+                const int s = it % S::ST;
+                const uint32_t phase = (it / S::ST) & 1;
+                if (!wait(full + 8 * s, phase) || !wait(sf_full + 8 * s, phase)) break;
+                tc::tc_fence_after();
+                const uint32_t sf = at_sf + s * S::SF, sfa = sft + s * S::SFC, sfb = sfa + 8;
 #pragma unroll
-            for (int j = 0; j < 4; j++)
+                for (int k = 0; k < 2; k++) {
+                    copy_scales(sfa + k * 4, sf + k * 512);
 #pragma unroll
-                for (int k = 0; k < 4; k++) sum[j][k] = fmaf(xt[i][ty * 4 + j], wt[i][tx + 16 * k], sum[j][k]);
-        __syncthreads();
+                    for (int h = 0; h < S::NB; h++) copy_scales(sfb + (k * S::NB + h) * 4, sf + 1024 * (1 + h) + k * 512);
+                }
+                const uint64_t ad = tc::sw128_kmajor_desc(at_a + s * S::A), bd = tc::sw128_kmajor_desc(at_b + s * S::B);
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    mma_mx4(tmem, tc::desc_advance(ad, j * 32), tc::desc_advance(bd, j * 32), idesc_mx4(NT, (j & 1) * 2),
+                            sfa + j / 2 * 4, sfb + j / 2 * 4 * S::NB, (it | j) != 0);
+                tc::mma_commit(empty + 8 * s);
+            }
+            tc::mma_commit(done);
+        }
+    } else if (warp >= 4) {
+        const int role = warp - 4;   // 0: weights' scales, 1 ..: tokens'
+        if (role <= S::NB) {
+            const uint8_t *src = role ? a.xs : a.ws;
+            const int vec = role ? a.xvec : a.wvec, row0 = role ? m0 + (role - 1) * 128 : o0;
+            const int last = (role ? a.m : a.out) - 1, rows = role ? min(NT, 128) : 128;
+            ScaleChunk now, next;
+            now.load(src, vec, row0, rows, last, a.groups, c0 * 16, lane);
+            for (int it = 0; it < stages; it += 2) {
+                if (it + 2 < stages) next.load(src, vec, row0, rows, last, a.groups, c0 * 16 + (it + 2) * 8, lane);
+                bool ok = true;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    if (it + h >= stages) break;
+                    const int s = (it + h) % S::ST;
+                    if (it + h >= S::ST) ok = wait(empty + 8 * s, ((it + h) / S::ST - 1) & 1);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    now.store(at_sf + s * S::SF + role * 1024, vec, h, lane);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(sf_full + 8 * s);
+                }
+                if (!ok) break;
+                now = next;
+            }
+        }
+        // the sums: a lane has an output, a column is a token's
+        const bool ok = __all_sync(~0u, wait(done, 0)) && !*abort;
+        tc::tc_fence_after();
+        const int o = o0 + role * 32 + lane;
+        const float f = a.s && o < a.out ? a.s[o] : 1.0f, b = a.b && o < a.out ? a.b[o] : 0.0f;
+        auto put = [&](int t, float v) {
+            if (t >= a.m || o >= a.out) return;
+            v = ok ? act_seq(fmaf(f, v, b), a.act) : __uint_as_float(0x7FFFFFFFu);
+            const long long i = (long long)t * a.ld_y + o;
+            if (a.dtype == FCM_BF16) static_cast<__nv_bfloat16 *>(a.y)[i] = __float2bfloat16_rn(v);
+            else if (a.dtype == FCM_F16) static_cast<__half *>(a.y)[i] = __float2half_rn(v);
+            else static_cast<float *>(a.y)[i] = v;
+        };
+        const uint32_t acc = tmem + ((uint32_t)role << 21);   // the warp's quarter of the lanes
+        if (a.split == 1) {
+            for (int c = 0; c < NT; c += 16) {
+                if (m0 + c >= a.m) break;
+                uint32_t r[16];
+                tc::tmem_ld16(acc + c, r);
+                tc::tmem_ld_wait(r, r);
+#pragma unroll
+                for (int i = 0; i < 16; i++) put(m0 + c + i, __uint_as_float(r[i]));
+            }
+        } else {
+            for (int c = 0; c < NT; c += 16) {
+                uint32_t r[16];
+                tc::tmem_ld16(acc + c, r);
+                tc::tmem_ld_wait(r, r);
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + i) * 128 + role * 32 + lane) * 4),
+                                 "r"(ok && stages > 0 ? r[i] : ok ? 0u : 0x7FFFFFFFu) : "memory");
+            }
+        }
+        tc::tc_fence_before();
+        if (a.split > 1) {
+            __syncwarp();
+            mx4_cluster_sync();
+            // each block of the cluster joins its share of the tokens, in the blocks' order
+            const int n0 = NT * (int)rank / a.split, n1 = NT * (int)(rank + 1) / a.split;
+            for (int c = n0; c < n1; c++) {
+                float v = 0.0f;
+                for (int r = 0; r < a.split; r++) {
+                    uint32_t addr;
+                    float p;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(base + (c * 128 + role * 32 + lane) * 4), "r"(r));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(addr) : "memory");
+                    v += p;
+                }
+                put(m0 + c, v);
+            }
+        }
     }
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const int t = m0 + ty * 4 + j, o = o0 + tx + 16 * k;
-            if (t < a.m && o < a.out)
-                static_cast<T *>(a.y)[(long long)t * a.ld_y + o] = Storage<T>::from_f(
-                    act_seq(fmaf(a.s ? a.s[o] : 1.0f, sum[j][k], a.b ? a.b[o] : 0.0f), a.act));
-        }
+    if (a.split > 1) {
+        __syncwarp();
+        if (warp < 4) mx4_cluster_sync();
+        mx4_cluster_sync();   // the others may still read this block's sums
+    }
+    __syncthreads();
+    if (warp == 2) tc::tmem_dealloc(tmem, S::COLS);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Rows of `bytes` bytes, `box` rows of 128 bytes at a time, 128-byte swizzled; what is past the end comes as zeros.
+static bool byte_map(CUtensorMap *map, const void *p, long long bytes, long long rows, int box) {
+    const cuuint64_t dim[2] = {(cuuint64_t)bytes, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)bytes};
+    const cuuint32_t size[2] = {128, (cuuint32_t)box}, step[2] = {1, 1};
+    const EncodeTiled enc = encode_tiled();
+    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dim, stride, size, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT>
+static cudaError_t run_mx4(Mx4MatmulArgs &a, const void *wq, const void *xq, int sms, cudaStream_t st) {
+    using S = Mx4Shape<NT>;
+    const long long bytes = a.groups * 16ll;
+    if (!byte_map(&a.wmap, wq, bytes, a.out, 128) || !byte_map(&a.xmap, xq, bytes, a.m, NT)) return cudaErrorInvalidValue;
+    static std::atomic<unsigned long long> attr{0};
+    const unsigned long long ctx = fcm_current_ctx_id();
+    if (ctx == 0 || attr.load(std::memory_order_relaxed) != ctx) {
+        const cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        attr.store(ctx, std::memory_order_relaxed);
+    }
+    const long long tiles = (long long)((a.m + NT - 1) / NT) * ((a.out + 127) / 128);
+    const int fit = S::COLS == 512 || S::SMEM > 113 * 1024 ? 1 : 2;
+    a.split = 1;
+    while (a.split < 8 && tiles * a.split * 2 <= (long long)sms * fit && 2 * a.split <= a.chunks) a.split *= 2;
+    return launch(mx4_matmul_kernel<NT>, dim3((unsigned)(tiles * a.split)), 256, S::SMEM, st, a, a.split);
 }
 
 }  // namespace seq
@@ -87,16 +352,20 @@ extern "C" fcm_status fcm_mx4_matmul(const fcm_mx4_matmul_desc *desc, const void
         return fcm_fail(FCM_ERR_INVALID_ARG, "xq or xs and y overlap");
     int sms;
     if ((st = seq::current_device(&sms)) != FCM_OK) return st;
-    const seq::Mx4MatmulArgs a = {static_cast<const uint8_t *>(xq), static_cast<const uint8_t *>(xs),
-                                  static_cast<const uint8_t *>(wq), static_cast<const uint8_t *>(ws), s, b, y, d.ld_y,
-                                  d.m, d.out, d.in, d.act};
+    const long long most = (((long long)d.m + 15) / 16) * ((d.out + 127) / 128);   // blocks of the smallest tiles
+    if (most * 8 > 0x7FFFFFFFLL) return fcm_fail(FCM_ERR_UNSUPPORTED, "m %d, out %d: above 2^31 - 1 blocks", d.m, d.out);
+    seq::Mx4MatmulArgs a = {};
+    a.ws = static_cast<const uint8_t *>(ws), a.xs = static_cast<const uint8_t *>(xs), a.s = s, a.b = b, a.y = y;
+    a.ld_y = d.ld_y, a.m = d.m, a.out = d.out, a.groups = (int)groups, a.act = d.act, a.dtype = d.dtype;
+    a.chunks = (int)((groups + 15) / 16);
+    a.wvec = seq::aligned16(ws) && groups % 16 == 0, a.xvec = seq::aligned16(xs) && groups % 16 == 0;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)((d.out + 63) / 64), (unsigned)((d.m + 63) / 64));
-    if (grid.y > 65535) return fcm_fail(FCM_ERR_UNSUPPORTED, "m %d above %d", d.m, 64 * 65535);
-    const cudaError_t ce = seq::launch(d.dtype == FCM_F32   ? seq::mx4_matmul_kernel<float>
-                                       : d.dtype == FCM_F16 ? seq::mx4_matmul_kernel<__half>
-                                                            : seq::mx4_matmul_kernel<__nv_bfloat16>,
-                                       grid, 256, 0, cs, a);
+    const long long tiles256 = (((long long)d.m + 255) / 256) * ((d.out + 127) / 128);
+    const cudaError_t ce = d.m <= 16    ? seq::run_mx4<16>(a, wq, xq, sms, cs)
+                           : d.m <= 32  ? seq::run_mx4<32>(a, wq, xq, sms, cs)
+                           : d.m <= 64  ? seq::run_mx4<64>(a, wq, xq, sms, cs)
+                           : d.m <= 128 || tiles256 < sms ? seq::run_mx4<128>(a, wq, xq, sms, cs)
+                                                          : seq::run_mx4<256>(a, wq, xq, sms, cs);
     if (ce != cudaSuccess) return fcm_fail(FCM_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(ce));
     return FCM_OK;
 }
