@@ -2,7 +2,9 @@
 // row.
 //
 //     S = e^G S;  u = B (v - S^T k);  S = S + k u^T;  y = scale S^T q
-#include "delta.cuh"
+#include <atomic>
+
+#include "delta_chunk.cuh"
 
 namespace fcm {
 namespace seq {
@@ -151,11 +153,31 @@ __global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const D
     }
 }
 
-template <typename T> static cudaError_t run_delta(const DeltaArgs &a, int sms, cudaStream_t st) {
+constexpr int kChunkedFrom = 16;   // longest sequence's rows from which prompts go in chunks
+
+template <typename T, int DK> static cudaError_t run_chunks(const DeltaArgs &a, dim3 grid, cudaStream_t st) {
+    static std::atomic<unsigned long long> attr{0};
+    const unsigned long long ctx = fcm_current_ctx_id();
+    if (ctx == 0 || attr.load(std::memory_order_relaxed) != ctx) {
+        const cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   DeltaChunk<DK>::SMEM);
+        if (e != cudaSuccess) return e;
+        attr.store(ctx, std::memory_order_relaxed);
+    }
+    return launch(delta_chunk_kernel<T, DK>, grid, DeltaChunk<DK>::THREADS, DeltaChunk<DK>::SMEM, st, a);
+}
+
+template <typename T> static cudaError_t run_delta(DeltaArgs a, cudaStream_t st) {
     const size_t v = 4 * sizeof(T);
     auto by = [](const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
     const bool vec = a.dv % 4 == 0 && by(a.state_in, 16) && by(a.state_out, 16) && by(a.y, v) && a.ld_y % 4 == 0;
     const dim3 grid((unsigned)((long long)a.q.n_seq * a.heads * a.slices));
+    if constexpr (sizeof(T) == 2) {
+        a.vec = by(a.qp, 16) && by(a.kp, 16) && ((a.ld_q | a.ld_k | a.dk) % 8) == 0;
+        a.vec_v = by(a.vp, 16) && ((a.ld_v | a.dv) % 8) == 0;
+        if (a.q.max_len >= kChunkedFrom && a.dk <= 128)
+            return a.dk <= 64 ? run_chunks<T, 64>(a, grid, st) : run_chunks<T, 128>(a, grid, st);
+    }
 #define ROWS(rk) launch(vec ? delta_row_kernel<T, rk, true> : delta_row_kernel<T, rk, false>, grid, 128, 0, st, a)
     return a.dk <= 64 ? ROWS(4) : a.dk <= 128 ? ROWS(8) : ROWS(16);
 #undef ROWS
@@ -229,9 +251,9 @@ extern "C" fcm_status fcm_gated_delta(const fcm_delta_desc *desc, const void *q,
     g.heads = d.heads, g.per_key = d.heads / d.key_heads, g.dk = d.dk, g.dv = d.dv;
     g.softplus = d.softplus, g.sigmoid = d.sigmoid, g.normalize = d.normalize, g.scale = d.scale;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t ce = d.dtype == FCM_F32   ? seq::run_delta<float>(g, sms, cs)
-                           : d.dtype == FCM_F16 ? seq::run_delta<__half>(g, sms, cs)
-                                                : seq::run_delta<__nv_bfloat16>(g, sms, cs);
+    const cudaError_t ce = d.dtype == FCM_F32   ? seq::run_delta<float>(g, cs)
+                           : d.dtype == FCM_F16 ? seq::run_delta<__half>(g, cs)
+                                                : seq::run_delta<__nv_bfloat16>(g, cs);
     if (ce != cudaSuccess) return fcm_fail(FCM_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(ce));
     return FCM_OK;
 }

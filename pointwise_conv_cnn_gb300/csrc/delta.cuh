@@ -22,6 +22,7 @@ struct DeltaArgs {
     int slices;                   // blocks of columns
     int softplus, sigmoid, normalize;
     float scale;
+    int vec, vec_v;   // eight keys and queries, values, of a row may be read at once
 };
 
 // G of one row and head, and its step B.  A scalar a row: the library's functions, whose errors are units of

@@ -44,7 +44,7 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
 // A block: 128 outputs of NT tokens.  Rows of the product are outputs, so that a warp's stores of a token are side by
 // side.  Inputs go in stages of 256, 128 bytes a row.
 template <int NT> struct Mx4Shape {
-    static constexpr int ST = NT == 128 ? 3 : 4;             // stages; two blocks an SM up to 128 tokens
+    static constexpr int ST = NT == 128 ? 3 : NT <= 32 ? 5 : 4;   // stages; two blocks an SM up to 128 tokens
     static constexpr int NB = (NT + 127) / 128;              // blocks of 128 tokens
     static constexpr int A = 128 * 128, B = NT * 128;        // bytes of a stage
     static constexpr int SF = 1024 * (1 + NB);               // of its scales: two words of four for each row
@@ -56,36 +56,35 @@ template <int NT> struct Mx4Shape {
 };
 
 // The 16 scale codes of `rows` rows for one chunk of 512 inputs, by a warp: on their way to shared memory as 4 blocks
-// (of 128 inputs) of 32 x 16 bytes, row r's word at (r % 32) * 16 + (r / 32) * 4.
-// Where rows of codes start at 16 bytes a lane has rows lane, lane + 32, .. whole, and stores 16 bytes a block.
-// Else four lanes have a row, a word each, taken from the two aligned words that it lies in.
+// (of 128 inputs) of 32 x 16 bytes, row r's word at (r % 32) * 16 + (r / 32) * 4.  Where rows of codes start at 16
+// bytes a lane has rows lane, lane + 32, .. whole, and stores 16 bytes a block.  Else four lanes have a row, a word
+// each, taken from the two aligned words that it lies in, which are put together only when they are stored: the
+// loads of the next chunk are under way meanwhile.
 struct ScaleChunk {
-    uint32_t w[16];
+    uint32_t lo[16], hi[16];
+    uint32_t shift, keep;
     __device__ __forceinline__ void load(const uint8_t *s, int vec, int row0, int rows, int last_row, int groups, int g0, int lane) {
         if (vec) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int r = min(row0 + i * 32 + lane, last_row);
-                const uint4 v = i * 32 < rows && g0 < groups
-                                    ? *reinterpret_cast<const uint4 *>(s + (size_t)r * groups + g0) : make_uint4(0, 0, 0, 0);
-                w[i] = v.x, w[4 + i] = v.y, w[8 + i] = v.z, w[12 + i] = v.w;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (i * 32 < rows) v = *reinterpret_cast<const uint4 *>(s + (size_t)min(row0 + i * 32 + lane, last_row) * groups + g0);
+                lo[i * 4] = v.x, lo[i * 4 + 1] = v.y, lo[i * 4 + 2] = v.z, lo[i * 4 + 3] = v.w;
             }
         } else {
             const int g = g0 + lane % 4 * 4, have = min(groups - g, 4);   // codes of this word
+            // rows 8 apart lie alike in their words; one past the last row is that row, and comes out as anything
+            shift = (uint32_t)(reinterpret_cast<uintptr_t>(s) + (size_t)(row0 + lane / 4) * groups + g) % 4 * 8;
+            keep = have >= 4 ? ~0u : have <= 0 ? 0u : (1u << (8 * have)) - 1;   // codes past the last: any number
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                const int r = min(row0 + i * 8 + lane / 4, last_row);
-                const uintptr_t at = reinterpret_cast<uintptr_t>(s + (size_t)r * groups + g);
-                const uint32_t off = at & 3;
+                const uintptr_t at = reinterpret_cast<uintptr_t>(s + (size_t)min(row0 + i * 8 + lane / 4, last_row) * groups + g);
+                const int off = (int)(at & 3);
                 const uint32_t *p = reinterpret_cast<const uint32_t *>(at - off);
-                uint32_t lo = 0, hi = 0;
-                if (i * 8 < rows && have > 0) lo = p[0];
-                if (i * 8 < rows && (int)off + have > 4) hi = p[1];
-                w[i] = __funnelshift_r(lo, hi, off * 8);
+                lo[i] = hi[i] = 0;
+                if (i * 8 < rows && have > 0) lo[i] = p[0];
+                if (i * 8 < rows && off + have > 4) hi[i] = p[1];
             }
-            const uint32_t keep = have >= 4 ? ~0u : have <= 0 ? 0u : (1u << (8 * have)) - 1;
-#pragma unroll
-            for (int i = 0; i < 16; i++) w[i] &= keep;   // codes past the last: any number, their values are 0
         }
     }
     // the blocks 2 * half and 2 * half + 1, one stage's
@@ -93,14 +92,15 @@ struct ScaleChunk {
         if (vec) {
 #pragma unroll
             for (int k = 0; k < 2; k++) {
-                if (half == 0) tc::sts128(to + k * 512 + lane * 16, w[k * 4], w[k * 4 + 1], w[k * 4 + 2], w[k * 4 + 3]);
-                else tc::sts128(to + k * 512 + lane * 16, w[8 + k * 4], w[9 + k * 4], w[10 + k * 4], w[11 + k * 4]);
+                if (half == 0) tc::sts128(to + k * 512 + lane * 16, lo[k], lo[4 + k], lo[8 + k], lo[12 + k]);
+                else tc::sts128(to + k * 512 + lane * 16, lo[2 + k], lo[6 + k], lo[10 + k], lo[14 + k]);
             }
         } else if ((lane & 2) == 2 * half) {
 #pragma unroll
             for (int i = 0; i < 16; i++) {
                 const int r = i * 8 + lane / 4;
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (lane & 1) * 512 + r % 32 * 16 + r / 32 * 4), "r"(w[i]) : "memory");
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (lane & 1) * 512 + r % 32 * 16 + r / 32 * 4),
+                             "r"(__funnelshift_r(lo[i], hi[i], shift) & keep) : "memory");
             }
         }
     }
@@ -108,6 +108,55 @@ struct ScaleChunk {
 
 __device__ __forceinline__ void mx4_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// N tokens' sums of output o as results.
+template <int N> __device__ __forceinline__ void mx4_values(const Mx4MatmulArgs &a, int o, float (&v)[N]) {
+    const float f = a.s ? a.s[o] : 1.0f, b = a.b ? a.b[o] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = fmaf(f, v[i], b);
+    if (a.act == FCM_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = silu(v[i]);
+    } else if (a.act != FCM_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = clamp_act(v[i], a.act);
+    }
+}
+
+// A lane's output of the block's tokens, from tensor memory; a warp's stores of a token are side by side.
+template <typename T, int NT>
+__device__ __forceinline__ void mx4_finish(const Mx4MatmulArgs &a, uint32_t acc, int o, int m0, bool ok) {
+    T *y = static_cast<T *>(a.y) + (long long)m0 * a.ld_y + o;
+    const bool mine = o < a.out;
+    const int last = min(o, a.out - 1);
+    for (int c = 0; c < NT && m0 + c < a.m; c += 16) {
+        uint32_t r[16];
+        float v[16];
+        tc::tmem_ld16(acc + c, r);
+        tc::tmem_ld_wait(r, r);
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] = __uint_as_float(ok ? r[i] : 0x7FFFFFFFu);
+        mx4_values<16>(a, last, v);
+        const int n = mine ? a.m - m0 - c : 0;
+        if (n >= 16) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) y[(c + i) * a.ld_y] = Storage<T>::from_f(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                if (i < n) y[(c + i) * a.ld_y] = Storage<T>::from_f(v[i]);
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void mx4_put(const Mx4MatmulArgs &a, int t, int o, int n, const float (&v)[8]) {
+    T *y = static_cast<T *>(a.y) + (long long)t * a.ld_y + o;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        if (i < n) y[i * a.ld_y] = Storage<T>::from_f(v[i]);
 }
 
 // Warp 0 asks for the factors (TMA), warp 1 multiplies, warps 4 to 6 bring the scales to shared memory, from where warp
@@ -194,14 +243,12 @@ template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const
             const uint8_t *src = role ? a.xs : a.ws;
             const int vec = role ? a.xvec : a.wvec, row0 = role ? m0 + (role - 1) * 128 : o0;
             const int last = (role ? a.m : a.out) - 1, rows = role ? min(NT, 128) : 128;
-            ScaleChunk now, next;
-            now.load(src, vec, row0, rows, last, a.groups, c0 * 16, lane);
-            for (int it = 0; it < stages; it += 2) {
-                if (it + 2 < stages) next.load(src, vec, row0, rows, last, a.groups, c0 * 16 + (it + 2) * 8, lane);
-                bool ok = true;
+            ScaleChunk chunk[2];
+            bool ok = true;
+            auto stage_pair = [&](const ScaleChunk &now, int it) {
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    if (it + h >= stages) break;
+                    if (it + h >= stages || !ok) break;
                     const int s = (it + h) % S::ST;
                     if (it + h >= S::ST) ok = wait(empty + 8 * s, ((it + h) / S::ST - 1) & 1);
                     ok = __all_sync(~0u, ok);
@@ -211,33 +258,26 @@ template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(sf_full + 8 * s);
                 }
-                if (!ok) break;
-                now = next;
+            };
+            auto load = [&](ScaleChunk &to, int it) {
+                if (it < stages) to.load(src, vec, row0, rows, last, a.groups, (2 * c0 + it) * 8, lane);
+            };
+            load(chunk[0], 0);
+            for (int it = 0; it < stages && ok; it += 4) {
+                load(chunk[1], it + 2);
+                stage_pair(chunk[0], it);
+                load(chunk[0], it + 4);
+                stage_pair(chunk[1], it + 2);
             }
         }
         // the sums: a lane has an output, a column is a token's
         const bool ok = __all_sync(~0u, wait(done, 0)) && !*abort;
         tc::tc_fence_after();
-        const int o = o0 + role * 32 + lane;
-        const float f = a.s && o < a.out ? a.s[o] : 1.0f, b = a.b && o < a.out ? a.b[o] : 0.0f;
-        auto put = [&](int t, float v) {
-            if (t >= a.m || o >= a.out) return;
-            v = ok ? act_seq(fmaf(f, v, b), a.act) : __uint_as_float(0x7FFFFFFFu);
-            const long long i = (long long)t * a.ld_y + o;
-            if (a.dtype == FCM_BF16) static_cast<__nv_bfloat16 *>(a.y)[i] = __float2bfloat16_rn(v);
-            else if (a.dtype == FCM_F16) static_cast<__half *>(a.y)[i] = __float2half_rn(v);
-            else static_cast<float *>(a.y)[i] = v;
-        };
         const uint32_t acc = tmem + ((uint32_t)role << 21);   // the warp's quarter of the lanes
         if (a.split == 1) {
-            for (int c = 0; c < NT; c += 16) {
-                if (m0 + c >= a.m) break;
-                uint32_t r[16];
-                tc::tmem_ld16(acc + c, r);
-                tc::tmem_ld_wait(r, r);
-#pragma unroll
-                for (int i = 0; i < 16; i++) put(m0 + c + i, __uint_as_float(r[i]));
-            }
+            if (a.dtype == FCM_BF16) mx4_finish<__nv_bfloat16, NT>(a, acc, o0 + role * 32 + lane, m0, ok);
+            else if (a.dtype == FCM_F16) mx4_finish<__half, NT>(a, acc, o0 + role * 32 + lane, m0, ok);
+            else mx4_finish<float, NT>(a, acc, o0 + role * 32 + lane, m0, ok);
         } else {
             for (int c = 0; c < NT; c += 16) {
                 uint32_t r[16];
@@ -246,7 +286,7 @@ template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const
 #pragma unroll
                 for (int i = 0; i < 16; i++)
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + i) * 128 + role * 32 + lane) * 4),
-                                 "r"(ok && stages > 0 ? r[i] : ok ? 0u : 0x7FFFFFFFu) : "memory");
+                                 "r"(ok ? r[i] : 0x7FFFFFFFu) : "memory");
             }
         }
         tc::tc_fence_before();
@@ -255,16 +295,26 @@ template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const
             mx4_cluster_sync();
             // each block of the cluster joins its share of the tokens, in the blocks' order
             const int n0 = NT * (int)rank / a.split, n1 = NT * (int)(rank + 1) / a.split;
-            for (int c = n0; c < n1; c++) {
-                float v = 0.0f;
+            const int o = o0 + role * 32 + lane;
+            for (int c = n0; c < n1 && m0 + c < a.m; c += 8) {
+                float v[8] = {};
                 for (int r = 0; r < a.split; r++) {
                     uint32_t addr;
-                    float p;
+                    float p[8];
                     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(base + (c * 128 + role * 32 + lane) * 4), "r"(r));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(addr) : "memory");
-                    v += p;
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[i]) : "r"(addr + min(i, n1 - 1 - c) * 512) : "memory");
+#pragma unroll
+                    for (int i = 0; i < 8; i++) v[i] += p[i];
                 }
-                put(m0 + c, v);
+                if (o < a.out) {
+                    const int n = min(n1 - c, a.m - m0 - c);
+                    mx4_values<8>(a, o, v);
+                    if (a.dtype == FCM_BF16) mx4_put<__nv_bfloat16>(a, m0 + c, o, n, v);
+                    else if (a.dtype == FCM_F16) mx4_put<__half>(a, m0 + c, o, n, v);
+                    else mx4_put<float>(a, m0 + c, o, n, v);
+                }
             }
         }
     }

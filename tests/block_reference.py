@@ -15,7 +15,9 @@ def gated_delta(q, k, v, dt, a, b, dt_bias, softplus, sigmoid, normalize, scale,
     errors of its own sums, of dk terms with the state and, in a chunk of rows, of up to 64 terms with
     other rows: U (dk + 256) times the terms' magnitudes, by Cauchy-Schwarz |k| |S| and |v|.  256 counts the
     64 terms, the products that make them (a chunk's inverse, decays, norms), and factors kept in two 16-bit parts,
-    2^-17 = 128 U.  e^G carries |G| times 12 U (softplus, product, sums of up to 64) and 4 U of its own."""
+    2^-17 = 128 U.  e^G carries |G| times 12 U (softplus, product, sums of up to 64) and 4 U of its own.  In a chunk y
+    is the sum of q.S, of the state before it, and of products with its rows' u, whose decayed sum `told` bounds;
+    for bf16 their factors may be kept in one f16 part: 2^-11 of the first's terms, and twice that of the others'."""
     tokens, hk, dk = q.shape
     heads, dv = v.shape[1:]
     per, c = heads // hk, U * (dk + 256)
@@ -26,7 +28,7 @@ def gated_delta(q, k, v, dt, a, b, dt_bias, softplus, sigmoid, normalize, scale,
         row = s if slot is None else int(slot[s])
         kept = 0 <= row < slots
         S = state[row].copy() if kept and state_in is not None else np.zeros((heads, dk, dv))
-        err = np.zeros((heads, dv))
+        err, told = np.zeros((heads, dv)), np.zeros((heads, dv))
         for t in range(at, at + length):
             qq, kk = np.repeat(q[t], per, 0), np.repeat(k[t], per, 0)
             if normalize:
@@ -47,9 +49,11 @@ def gated_delta(q, k, v, dt, a, b, dt_bias, softplus, sigmoid, normalize, scale,
             off_u = np.abs(B)[:, None] * (c * (np.abs(v[t]) + nk * size) + nk * off) + 8.0 * U * np.abs(u)
             rho = decay * np.maximum(1.0, np.abs(1.0 - B[:, None] * nk * nk))
             err = rho * err + off + nk * off_u + c * nk * np.abs(u)
+            told = decay * told + nk * np.abs(u)
             size = np.sqrt((S * S).sum(1))
             y[t] = np.einsum("hk,hkv->hv", qq, S)
-            e[t] = stored(y[t], nq * (err + c * size + c * nk * np.abs(u)), dtype)
+            part = 2.0 ** -11 * (size + 3.0 * told) if dtype == "bf16" else 0.0   # |S before| <= |S| + told
+            e[t] = stored(y[t], nq * (err + c * size + c * nk * np.abs(u) + part), dtype)
         if kept:
             state[row] = S
             e_state[row] = err[:, None] + U * np.abs(S).max(1, keepdims=True)
