@@ -15,22 +15,22 @@ namespace seq {
 
 template <int DK> struct DeltaChunk {
     static constexpr int C = 32;                      // rows of a chunk
-    static constexpr int DS = DK / 32;                // warps that share 16 columns' states, 32 keys each
+    static constexpr int DS = 2, KW = DK / DS;        // warps that share 16 columns' states, keys of each
     static constexpr int STATE = 2 * DS, FRONT = 4;   // warps
     static constexpr int THREADS = 32 * (STATE + FRONT + 1);
     static constexpr int SLOTS = 3;
     static constexpr int KS = 2 * DK + 16;            // bytes of a row of keys: eight rows in different banks
-    static constexpr int TS = 80;                     // of T and of the rows' products P
-    static constexpr int VS = 80;                     // of values
-    static constexpr int AS = 36;                     // floats of a row of A
+    static constexpr int TS = 80;                     // of T's and the rows' products' 16-bit parts, and of values
+    static constexpr int AS = 36;                     // floats of a row of A, and of T on its way
     // a slot's parts, bytes
-    static constexpr int Q = C * KS, V = 2 * C * KS, THI = V + C * VS, TLO = THI + C * TS, PHI = TLO + C * TS,
-                         PLO = PHI + C * TS, A = PLO + C * TS, SC = A + C * AS * 4, SLOT = SC + 12 * C * 4;
+    static constexpr int Q = C * KS, V = 2 * C * KS, TP = V + C * TS, PP = TP + 3 * C * TS, A = PP + 2 * C * TS,
+                         SC = A + C * AS * 4, SLOT = SC + 8 * C * 4;
     static constexpr int XCH = 2 * 2 * DS * 8 * 512;   // sums on their way between warps: [turn][16 columns][warp][16 bytes][lane]
-    static constexpr int SMEM = SLOTS * SLOT + XCH;
+    static constexpr int TMP = C * AS * 4;             // T's diagonal blocks
+    static constexpr int SMEM = SLOTS * SLOT + XCH + TMP;
 };
-// A slot's factors by row
-enum { kBeta, kBetaReach, kQReach, kToEnd, kTDown, kPDown, kFk, kFq, kSumHi, kSumLo, kTotal };
+// A slot's factors by row: B and B e^c / |k| (for x), e^c / |q| scale (y), e^(c_last - c) / |k| (the states).
+enum { kXy = 0 /* two a row */, kQReach = 2, kToEnd, kSumHi, kSumLo, kBeta, kTotal };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -40,8 +40,13 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void mma_half(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+template <typename T> __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -67,10 +72,29 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
     hi = *reinterpret_cast<const uint32_t *>(&h), lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// N tiles of 16 x 8 sums as the left factors of the next product, in two parts, each of a lane's two rows times a
-// power of two that its four lanes agree on; `down` undoes it.  Tiles 2 i and 2 i + 1 are 16 inner places.
+// Two numbers in three parts of bf16, by cutting: the top 16 bits, those of what is left, and the rest, exactly.
+__device__ __forceinline__ void cut(float &a, float &b, uint32_t &part) {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    part = __byte_perm(x, y, 0x7632);
+    a -= __uint_as_float(x & 0xFFFF0000u), b -= __uint_as_float(y & 0xFFFF0000u);
+}
+// N tiles of 16 x 8 sums as the left factors of the next product, in M parts of bf16.  Tiles 2 i and 2 i + 1 are 16
+// inner places.
+template <int M, int N> __device__ __forceinline__ void as_bf16(const float (&c)[N][4], uint32_t (&part)[3][N / 2][4]) {
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            float a = c[i][2 * r], b = c[i][2 * r + 1];
+#pragma unroll
+            for (int m = 0; m < M; m++) cut(a, b, part[m][i / 2][i % 2 * 2 + r]);
+        }
+}
+
+// The same in two parts of f16, each of a lane's two rows times a power of two that its four lanes agree on;
+// `down` undoes it.
 template <int N>
-__device__ __forceinline__ void as_factor(const float (&c)[N][4], uint32_t (&hi)[N / 2][4], uint32_t (&lo)[N / 2][4], float (&down)[2]) {
+__device__ __forceinline__ void as_half(const float (&c)[N][4], uint32_t (&part)[3][N / 2][4], float (&down)[2]) {
     uint32_t top[2] = {};
 #pragma unroll
     for (int i = 0; i < N; i++)
@@ -88,7 +112,7 @@ __device__ __forceinline__ void as_factor(const float (&c)[N][4], uint32_t (&hi)
     for (int i = 0; i < N; i++)
 #pragma unroll
         for (int r = 0; r < 2; r++)
-            split2(c[i][2 * r] * up[r], c[i][2 * r + 1] * up[r], hi[i / 2][i % 2 * 2 + r], lo[i / 2][i % 2 * 2 + r]);
+            split2(c[i][2 * r] * up[r], c[i][2 * r + 1] * up[r], part[0][i / 2][i % 2 * 2 + r], part[1][i / 2][i % 2 * 2 + r]);
 }
 
 // Eight neighbouring keys or queries of a row, zeros past the row's end.
@@ -104,22 +128,29 @@ template <typename T> __device__ __forceinline__ uint4 load_keys(const T *p, int
     return v;
 }
 
+// 16 bytes from global to shared memory without a register; zeros where there is no row.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
+}
+
 // One block: 32 value columns of a head.
 //
-// The states stay in registers, transposed: a warp has 16 columns by 32 keys as the sums of a 16 x 8 x 16 product, and
-// sums are laid out as the left factors of the next, so that x, u and the states go from product to product without
-// leaving their lanes; only the warps' parts of S^T k and S^T q, over 32 keys each, meet in shared memory.
-// Four warps go ahead: they read rows, bring keys and queries to 16 bits of f16 (16-bit types are exact in it after a
-// power of two a row, but for parts below 2^-24 of the row's length), and make A and the products P of queries and keys with
-// their decays.  One inverts 1 + A by forward substitution, a column a lane, in 32 bits.
+// The states stay in registers, transposed: a warp has 16 columns by half the keys as the sums of 16 x 8 x 16 products,
+// and sums are laid out as the left factors of the next, so that x, u and the states go from product to product without
+// leaving their lanes; only the two halves of S^T k and S^T q meet in shared memory.  Four warps go ahead: they ask for
+// rows, which enter products as they are stored, and make A and the products P of queries and keys with their decays; the
+// rows' lengths are the products of keys and of queries with themselves.  One inverts 1 + A: two blocks of 16 by forward
+// substitution, a column a lane, and the block below them by two products, in 32 bits.
 //
-// Rounding: keys and queries are used as they are, and their lengths, decays and steps applied to sums in 32 bits.  S, x
-// and u enter products in two f16 parts, 22 bits, and T too; the parts' products that are left out are below 2^-22 of a
-// sum's terms.  What only y needs (S^T q, P u) has one part, 2^-12, where y has bf16's 2^-9, and two where it is f16.
+// Rounding: keys and queries are used as they are, and their lengths, decays and steps applied to sums in 32 bits.  x, u
+// and T enter products in three bf16 parts, which hold all 24 bits, and so do S and the decayed u beside bf16 keys; beside
+// f16 keys they have two f16 parts, 22 bits.  Products of parts below 2^-23 are left out.  What only y needs (S^T q, P u)
+// has two parts, 2^-16 at least, where y keeps 2^-9 or 2^-12.
 template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::THREADS, 1) delta_chunk_kernel(const DeltaArgs a) {
     using D = DeltaChunk<DK>;
-    constexpr int C = D::C, DS = D::DS, NT = 4;            // tiles of 8 keys of a warp, and of 8 rows of a chunk
-    constexpr bool FINE = std::is_same<T, __half>::value;
+    using B = __nv_bfloat16;
+    constexpr int C = D::C, DS = D::DS, NS = D::KW / 8, NC = C / 8;   // tiles of 8 keys of a warp, of 8 rows of a chunk
+    constexpr bool HALF = std::is_same<T, __half>::value;
     constexpr int kFull = 1, kInv = 4, kFree = 7, kMeet = 10, kTeam = 12;   // barriers; the first three by slot
     constexpr int ALL = D::THREADS, STATE = 32 * D::STATE, FRONT = 32 * D::FRONT;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -137,67 +168,57 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
 
     if (warp >= D::STATE && warp < D::STATE + D::FRONT) {
         // ---- ahead: rows to factors
-        constexpr int VPR = DK / 8, RPP = FRONT / VPR, PASS = C / RPP;   // lanes of a row, rows at a time
+        constexpr int VPR = DK / 8, RPP = FRONT / VPR, PASS = C / RPP;   // 16-byte pieces of a row, rows at a time
         const int tid = threadIdx.x - STATE, w = warp - D::STATE, col = tid % VPR * 8, r0 = tid / VPR;
         const T *kp = static_cast<const T *>(a.kp) + (size_t)g * a.dk, *qp = static_cast<const T *>(a.qp) + (size_t)g * a.dk;
         const T *vp = static_cast<const T *>(a.vp) + (size_t)h * a.dv + d0;
-        const T *dtp = static_cast<const T *>(a.dt) + h, *bp = static_cast<const T *>(a.b) + h;
+        const int vcols = min(a.dv - d0, kDeltaCols), vc = tid % 4 * 8;
         const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-        uint4 kr[PASS], qr[PASS], vr;
         float dt = 0.0f, bv = 0.0f;
         auto load = [&](int c) {
+            const uint32_t to = base + c % D::SLOTS * D::SLOT;
+            unsigned char *plain = smem + c % D::SLOTS * D::SLOT;
 #pragma unroll
             for (int p = 0; p < PASS; p++) {
-                const int i = c * C + r0 + p * RPP;
-                const bool live = i < len;
-                const long long t = t0 + i;
-                kr[p] = load_keys(kp + t * a.ld_k, col, a.dk, live, a.vec);
-                qr[p] = load_keys(qp + t * a.ld_q, col, a.dk, live, a.vec);
+                const int row = r0 + p * RPP;
+                const bool live = c * C + row < len;
+                const long long t = live ? t0 + c * C + row : t0;
+                const int at = row * D::KS + col * 2;
+                if (a.vec) {
+                    const int e = col < a.dk ? col : 0;
+                    copy16(to + at, kp + t * a.ld_k + e, live && col < a.dk);
+                    copy16(to + D::Q + at, qp + t * a.ld_q + e, live && col < a.dk);
+                } else {
+                    *reinterpret_cast<uint4 *>(plain + at) = load_keys(kp + t * a.ld_k, col, a.dk, live, false);
+                    *reinterpret_cast<uint4 *>(plain + D::Q + at) = load_keys(qp + t * a.ld_q, col, a.dk, live, false);
+                }
             }
-            const int i = c * C + tid / 4;
-            vr = load_keys(vp + (t0 + i) * a.ld_v, tid % 4 * 8, min(a.dv - d0, kDeltaCols), i < len, a.vec_v);
-            if (w == 0) {
-                const bool live = c * C + lane < len;
-                dt = live ? Storage<T>::to_f(dtp[(t0 + c * C + lane) * a.ld_dt]) : 0.0f;
-                bv = live ? Storage<T>::to_f(bp[(t0 + c * C + lane) * a.ld_b]) : 0.0f;
-            }
+            const bool live = c * C + tid / 4 < len;
+            const T *v = vp + (live ? t0 + c * C + tid / 4 : t0) * a.ld_v;
+            const int at = D::V + tid / 4 * D::TS + vc * 2;
+            if (a.vec_v) copy16(to + at, v + (vc < vcols ? vc : 0), live && vc < vcols);
+            else *reinterpret_cast<uint4 *>(plain + at) = load_keys(v, vc, vcols, live, false);
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        if (chunks) load(0);
+        auto load_scalars = [&](int c) {
+            const bool live = c * C + lane < len;
+            dt = live ? Storage<T>::to_f(static_cast<const T *>(a.dt)[(t0 + c * C + lane) * a.ld_dt + h]) : 0.0f;
+            bv = live ? Storage<T>::to_f(static_cast<const T *>(a.b)[(t0 + c * C + lane) * a.ld_b + h]) : 0.0f;
+        };
+        if (chunks) {
+            load(0);
+            if (w == 0) load_scalars(0);
+        }
         for (int c = 0; c < chunks; c++) {
             const int slot = c % D::SLOTS;
-            if (c >= D::SLOTS) bar_sync(kFree + slot, STATE + FRONT);
             unsigned char *at = smem + slot * D::SLOT;
             float *f = factors(slot);
-#pragma unroll
-            for (int p = 0; p < PASS; p++)
-#pragma unroll
-                for (int which = 0; which < 2; which++) {
-                    const uint4 raw = which ? qr[p] : kr[p];
-                    const T *e = reinterpret_cast<const T *>(&raw);
-                    float v[8], sq = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; i++) v[i] = Storage<T>::to_f(e[i]), sq = fmaf(v[i], v[i], sq);
-#pragma unroll
-                    for (int m = 1; m < VPR; m <<= 1) sq += __shfl_xor_sync(~0u, sq, m);
-                    const int row = r0 + p * RPP;
-                    float down = 1.0f;
-                    uint4 out = raw;
-                    if (!FINE) {   // a row of length 1 to 2 times a power of two
-                        const int half = ((int)(__float_as_uint(sq) >> 23) - 127) >> 1;
-                        const float up = __uint_as_float((uint32_t)(127 - half) << 23);
-                        down = __uint_as_float((uint32_t)(127 + half) << 23);
-                        __half2 o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) o[i] = __floats2half2_rn(v[2 * i] * up, v[2 * i + 1] * up);
-                        out = *reinterpret_cast<const uint4 *>(o);
-                    }
-                    *reinterpret_cast<uint4 *>(at + which * D::Q + row * D::KS + col * 2) = out;
-                    if (col == 0) {
-                        const float norm = (a.normalize ? rsqrtf(sq + kDeltaEps) : 1.0f) * down;
-                        f[(which ? kFq : kFk) * C + row] = which ? norm * a.scale : norm;
-                    }
-                }
-            *reinterpret_cast<uint4 *>(at + D::V + tid / 4 * D::VS + tid % 4 * 16) = vr;
+            if (c + 1 < chunks) {
+                if (c + 1 >= D::SLOTS) bar_sync(kFree + (c + 1) % D::SLOTS, STATE + FRONT);
+                load(c + 1);
+            } else {
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
             if (w == 0) {
                 const bool live = c * C + lane < len;
                 float G = log_decay(dt + bias, av, a.softplus);
@@ -211,74 +232,78 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 const float hi = (float)sum;
                 f[kSumHi * C + lane] = hi, f[kSumLo * C + lane] = (float)(sum - hi);
                 f[kBeta * C + lane] = live ? step_of(bv, a.sigmoid) : 0.0f;
+                if (c + 1 < chunks) load_scalars(c + 1);
             }
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             bar_sync(kTeam, FRONT);
-            if (c + 1 < chunks) load(c + 1);
-            // products of keys (warps 0, 2) and of queries with keys (1, 3): rows 16 .. 31 (0, 1), 0 .. 15 (2, 3)
+            // products of keys (warps 0, 2) and of queries with keys (1, 3): rows 16 .. 31 (0, 1), 0 .. 15 (2, 3); and of
+            // those rows with themselves
             const int m0 = w < 2 ? 16 : 0;
             const bool queries = w & 1;
-            const uint32_t ka = base + slot * D::SLOT;
-            float s[4][4] = {};
+            const uint32_t ka = base + slot * D::SLOT, qa = ka + (queries ? D::Q : 0);
+            float s[4][4] = {}, own[2][4] = {};
 #pragma unroll
             for (int kk = 0; kk < DK / 16; kk++) {
-                uint32_t am[4], b[2][4];
-                ldsm4(am, ka + (queries ? D::Q : 0) + (m0 + lane % 16) * D::KS + kk * 32 + lane / 16 * 16);
-#pragma unroll
-                for (int n = 0; n < 2; n++) {
-                    if (n == 1 && m0 == 0) break;
-                    ldsm4(b[n], ka + (n * 16 + lane / 16 * 8 + lane % 8) * D::KS + kk * 32 + lane / 8 % 2 * 16);
-                    mma_half(s[2 * n], am, b[n][0], b[n][1]);
-                    mma_half(s[2 * n + 1], am, b[n][2], b[n][3]);
+                uint32_t am[4], b[4];
+                ldsm4(am, qa + (m0 + lane % 16) * D::KS + kk * 32 + lane / 16 * 16);
+                const uint32_t p = (lane / 16 * 8 + lane % 8) * D::KS + kk * 32 + lane / 8 % 2 * 16;
+                ldsm4(b, ka + p);
+                mma16<T>(s[0], am, b[0], b[1]);
+                mma16<T>(s[1], am, b[2], b[3]);
+                if (m0) {
+                    ldsm4(b, ka + 16 * D::KS + p);
+                    mma16<T>(s[2], am, b[0], b[1]);
+                    mma16<T>(s[3], am, b[2], b[3]);
                 }
+                ldsm4(b, qa + m0 * D::KS + p);
+                mma16<T>(own[0], am, b[0], b[1]);
+                mma16<T>(own[1], am, b[2], b[3]);
             }
             const int i0 = m0 + lane / 4, j0 = lane % 4 * 2;
-            float hi_i[2], lo_i[2], fi[2];
+            // the rows' own products, of row i with i: rows 0 .. 7 in tile 0, 8 .. 15 in tile 1
+            float fi[2];
 #pragma unroll
             for (int r = 0; r < 2; r++) {
-                const int i = i0 + 8 * r;
-                hi_i[r] = f[kSumHi * C + i], lo_i[r] = f[kSumLo * C + i];
-                fi[r] = queries ? f[kFq * C + i] : f[kBeta * C + i] * f[kFk * C + i];
+                const float mine = lane / 4 % 2 ? own[r][2 * r + 1] : own[r][2 * r];
+                const float sq = __shfl_sync(~0u, mine, lane / 4 * 4 + lane / 8);
+                fi[r] = a.normalize ? rsqrtf(sq + kDeltaEps) : 1.0f;
+                if (lane % 4 == 0) f[(queries ? kQReach : kToEnd) * C + i0 + 8 * r] = queries ? fi[r] * a.scale : fi[r];
             }
-            uint32_t top[2] = {};
+            bar_sync(kTeam, FRONT);
+            float hi_i[2], lo_i[2];
 #pragma unroll
-            for (int n = 0; n < 4; n++)
+            for (int r = 0; r < 2; r++) {
+                hi_i[r] = f[kSumHi * C + i0 + 8 * r], lo_i[r] = f[kSumLo * C + i0 + 8 * r];
+                fi[r] *= queries ? a.scale : f[kBeta * C + i0 + 8 * r];
+            }
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int r = e / 2, i = i0 + 8 * r, j = n * 8 + j0 + e % 2;
-                    const float d = (hi_i[r] - f[kSumHi * C + j]) + (lo_i[r] - f[kSumLo * C + j]);
-                    const bool in = queries ? j <= i : j < i;
-                    s[n][e] = in ? s[n][e] * fi[r] * f[kFk * C + j] * ex2(kLog2e * d) : 0.0f;
-                    top[r] = max(top[r], magnitude(s[n][e]));
-                }
-            if (!queries) {
-                float *A = reinterpret_cast<float *>(at + D::A);
-#pragma unroll
-                for (int n = 0; n < 4; n++)
-#pragma unroll
-                    for (int r = 0; r < 2; r++)
-                        *reinterpret_cast<float2 *>(A + (i0 + 8 * r) * D::AS + n * 8 + j0) = make_float2(s[n][2 * r], s[n][2 * r + 1]);
-            } else {
+            for (int n = 0; n < 4; n++) {
+                const float2 hj = *reinterpret_cast<const float2 *>(f + kSumHi * C + n * 8 + j0);
+                const float2 lj = *reinterpret_cast<const float2 *>(f + kSumLo * C + n * 8 + j0);
+                const float2 kj = *reinterpret_cast<const float2 *>(f + kToEnd * C + n * 8 + j0);
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
-                    top[r] = max(top[r], __shfl_xor_sync(~0u, top[r], 1));
-                    top[r] = max(top[r], __shfl_xor_sync(~0u, top[r], 2));
-                    const Power p(top[r]);
-                    const int i = i0 + 8 * r;
-                    if (lane % 4 == 0) f[kPDown * C + i] = p.down;
-#pragma unroll
-                    for (int n = 0; n < 4; n++) {
-                        uint32_t hi, lo;
-                        split2(s[n][2 * r] * p.up, s[n][2 * r + 1] * p.up, hi, lo);
-                        *reinterpret_cast<uint32_t *>(at + D::PHI + i * D::TS + n * 16 + j0 * 2) = hi;
-                        if (FINE) *reinterpret_cast<uint32_t *>(at + D::PLO + i * D::TS + n * 16 + j0 * 2) = lo;
+                    const int i = i0 + 8 * r, j = n * 8 + j0, last = queries ? i : i - 1;
+                    const float x = s[n][2 * r] * fi[r] * kj.x * ex2(kLog2e * ((hi_i[r] - hj.x) + (lo_i[r] - lj.x)));
+                    const float y = s[n][2 * r + 1] * fi[r] * kj.y * ex2(kLog2e * ((hi_i[r] - hj.y) + (lo_i[r] - lj.y)));
+                    float2 v = make_float2(j <= last ? x : 0.0f, j + 1 <= last ? y : 0.0f);
+                    if (!queries) {
+                        *reinterpret_cast<float2 *>(at + D::A + (i * D::AS + j) * 4) = v;
+                    } else {
+                        uint32_t part;
+                        cut(v.x, v.y, part);
+                        *reinterpret_cast<uint32_t *>(at + D::PP + i * D::TS + j * 2) = part;
+                        cut(v.x, v.y, part);
+                        *reinterpret_cast<uint32_t *>(at + D::PP + C * D::TS + i * D::TS + j * 2) = part;
                     }
                 }
             }
-            if (w == 2) {   // rows' factors
-                const float hi = f[kSumHi * C + lane], lo = f[kSumLo * C + lane];
-                const float reach = ex2(kLog2e * hi) * (1.0f + lo), fk = f[kFk * C + lane];
-                f[kBetaReach * C + lane] = f[kBeta * C + lane] * reach * fk;
-                f[kQReach * C + lane] = f[kFq * C + lane] * reach;
+            bar_sync(kTeam, FRONT);   // all have read the rows' lengths, which become the rows' factors
+            if (w == 2) {
+                const float hi = f[kSumHi * C + lane], lo = f[kSumLo * C + lane], beta = f[kBeta * C + lane];
+                const float reach = ex2(kLog2e * hi) * (1.0f + lo), fk = f[kToEnd * C + lane];
+                *reinterpret_cast<float2 *>(f + kXy * C + 2 * lane) = make_float2(beta, beta * reach * fk);
+                f[kQReach * C + lane] *= reach;
                 f[kToEnd * C + lane] = fk * ex2(kLog2e * ((f[kSumHi * C + C - 1] - hi) + (f[kSumLo * C + C - 1] - lo)));
                 if (lane == C - 1) f[kTotal * C] = reach;
             }
@@ -287,189 +312,251 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
         return;
     }
     if (warp == D::STATE + D::FRONT) {
-        // ---- the inverse: row i of a column is that of 1 less the rows above it, by A
+        // ---- the inverse.  A column of a diagonal block a lane: row i is that of 1 less the rows above it, by A.
+        float *own = reinterpret_cast<float *>(smem + D::SLOTS * D::SLOT + D::XCH);
+        const int j = lane % 16, half = lane / 16;
         for (int c = 0; c < chunks; c++) {
             const int slot = c % D::SLOTS;
             bar_sync(kFull + slot, ALL);
             const float *A = reinterpret_cast<const float *>(smem + slot * D::SLOT + D::A);
-            float t[C];
+            unsigned char *to = smem + slot * D::SLOT + D::TP;
+            auto put = [&](int i, int col, float v) {   // in three parts
 #pragma unroll
-            for (int i = 0; i < C; i++) {
-                float s[4] = {lane == i ? 1.0f : 0.0f};
+                for (int m = 0; m < 3; m++) {
+                    const uint32_t x = __float_as_uint(v);
+                    *reinterpret_cast<unsigned short *>(to + m * C * D::TS + i * D::TS + col * 2) = (unsigned short)(x >> 16);
+                    v -= __uint_as_float(x & 0xFFFF0000u);
+                }
+            };
+            float t[16];
+            const float *Ad = A + 16 * half * (D::AS + 1);
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                float s[2] = {j == i ? 1.0f : 0.0f};
 #pragma unroll
                 for (int m = 0; m < i; m += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(A + i * D::AS + m);
+                    const float4 v = *reinterpret_cast<const float4 *>(Ad + i * D::AS + m);
                     const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int k = 0; k < 4; k++)
-                        if (m + k < i) s[k] = fmaf(-e[k], t[m + k], s[k]);
+                        if (m + k < i) s[k & 1] = fmaf(-e[k], t[m + k], s[k & 1]);
                 }
-                t[i] = (s[0] + s[1]) + (s[2] + s[3]);
+                t[i] = s[0] + s[1];
+                own[(16 * half + i) * D::AS + j] = t[i];
+                put(16 * half + i, 16 * half + j, t[i]);
             }
-            __half *hi = reinterpret_cast<__half *>(smem + slot * D::SLOT + D::THI), *lo = reinterpret_cast<__half *>(smem + slot * D::SLOT + D::TLO);
-            float mine = 0.0f;
+            __syncwarp();
+            // below them: -T22 (A21 T11), eight rows a half of the lanes
+            float x[16];
 #pragma unroll
-            for (int i = 0; i < C; i++) {
-                const Power p(__reduce_max_sync(~0u, magnitude(t[i])));
-                const float v = t[i] * p.up;
-                const __half x = __float2half_rn(v);
-                hi[i * (D::TS / 2) + lane] = x;
-                lo[i * (D::TS / 2) + lane] = __float2half_rn(v - __half2float(x));
-                if (lane == i) mine = p.down;
+            for (int m = 0; m < 16; m++) x[m] = own[m * D::AS + j];
+            float p[16];
+            auto rows = [&](const float *from, float (&out)[8]) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    float s[2] = {};
+#pragma unroll
+                    for (int m = 0; m < 16; m += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(from + (8 * half + i) * D::AS + m);
+                        s[0] = fmaf(v.x, x[m], s[0]), s[1] = fmaf(v.y, x[m + 1], s[1]);
+                        s[0] = fmaf(v.z, x[m + 2], s[0]), s[1] = fmaf(v.w, x[m + 3], s[1]);
+                    }
+                    out[i] = s[0] + s[1];
+                }
+            };
+            float r[8];
+            rows(A + 16 * D::AS, r);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float other = __shfl_xor_sync(~0u, r[i], 16);
+                p[i] = half ? other : r[i], p[8 + i] = half ? r[i] : other;
             }
-            factors(slot)[kTDown * C + lane] = mine;
+#pragma unroll
+            for (int m = 0; m < 16; m++) x[m] = p[m];
+            rows(own + 16 * D::AS, r);
+#pragma unroll
+            for (int i = 0; i < 8; i++) put(16 + 8 * half + i, j, -r[i]);
+            __syncwarp();
             bar_arrive(kInv + slot, STATE + 32);
         }
         return;
     }
     // ---- the states
-    const int pair = warp / DS, part = warp % DS;           // 16 columns, 32 keys
-    const int rd = pair * 16 + lane / 4, k0 = part * 32;    // a lane's columns rd and rd + 8 of the block's
+    const int pair = warp / DS, part = warp % DS;                 // 16 columns, half the keys
+    const int rd = pair * 16 + lane / 4, k0 = part * D::KW;       // a lane's columns rd and rd + 8 of the block's
     const int row = a.state_in || a.state_out ? state_row(a.q, q) : -1;
     const size_t cell = ((size_t)max(row, 0) * a.heads + h) * a.dk * a.dv + d0;
-    float S[NT][4];
+    float S[NS][4];
 #pragma unroll
-    for (int n = 0; n < NT; n++)
+    for (int n = 0; n < NS; n++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             const int k = k0 + n * 8 + lane % 4 * 2 + e % 2, d = rd + e / 2 * 8;
             S[n][e] = a.state_in && row >= 0 && k < a.dk && d0 + d < a.dv ? a.state_in[cell + (size_t)k * a.dv + d] : 0.0f;
         }
     const uint32_t meet = base + D::SLOTS * D::SLOT + pair * DS * 8 * 512 + lane * 16;
-    T *y = static_cast<T *>(a.y) + (size_t)h * a.dv + d0;
+    T *y = static_cast<T *>(a.y) + (size_t)h * a.dv + d0 + rd;
+    const bool in0 = d0 + rd < a.dv, in1 = d0 + rd + 8 < a.dv;
     for (int c = 0; c < chunks; c++) {
         const int slot = c % D::SLOTS;
         const uint32_t at = base + slot * D::SLOT;
         const float *f = factors(slot);
-        uint32_t hi[NT / 2][4], lo[NT / 2][4];
-        float down[2];
-        as_factor(S, hi, lo, down);
-        bar_sync(kFull + slot, ALL);
-        float sk[NT][4] = {}, sq[NT][4] = {};
+        float sk[NC][4] = {}, sq[NC][4] = {};
+        {
+            uint32_t sp[3][NS / 2][4];
+            float down[2] = {1.0f, 1.0f};
+            if constexpr (HALF) as_half(S, sp, down);
+            else as_bf16<3>(S, sp);
+            bar_sync(kFull + slot, ALL);
 #pragma unroll
-        for (int kk = 0; kk < 2; kk++)
+            for (int kk = 0; kk < NS / 2; kk++)
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t b[4];
-                const uint32_t p = at + (n * 8 + lane / 16 * 8 + lane % 8) * D::KS + (k0 + kk * 16 + lane / 8 % 2 * 8) * 2;
-                ldsm4(b, p);
-                mma_half(sk[n], hi[kk], b[0], b[1]);
-                mma_half(sk[n + 1], hi[kk], b[2], b[3]);
-                mma_half(sk[n], lo[kk], b[0], b[1]);
-                mma_half(sk[n + 1], lo[kk], b[2], b[3]);
-                ldsm4(b, p + D::Q);
-                mma_half(sq[n], hi[kk], b[0], b[1]);
-                mma_half(sq[n + 1], hi[kk], b[2], b[3]);
-                if (FINE) {
-                    mma_half(sq[n], lo[kk], b[0], b[1]);
-                    mma_half(sq[n + 1], lo[kk], b[2], b[3]);
+                for (int n = 0; n < NC; n += 2) {
+                    uint32_t b[4];
+                    const uint32_t p = at + (n * 8 + lane / 16 * 8 + lane % 8) * D::KS + (k0 + kk * 16 + lane / 8 % 2 * 8) * 2;
+                    ldsm4(b, p);
+#pragma unroll
+                    for (int m = 0; m < (HALF ? 2 : 3); m++) {
+                        mma16<T>(sk[n], sp[m][kk], b[0], b[1]);
+                        mma16<T>(sk[n + 1], sp[m][kk], b[2], b[3]);
+                    }
+                    ldsm4(b, p + D::Q);
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        mma16<T>(sq[n], sp[m][kk], b[0], b[1]);
+                        mma16<T>(sq[n + 1], sp[m][kk], b[2], b[3]);
+                    }
                 }
-            }
+            if (HALF)
+#pragma unroll
+                for (int n = 0; n < NC; n++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) sk[n][e] *= down[e / 2], sq[n][e] *= down[e / 2];
+        }
+        // the halves meet: all of S^T k, and of S^T q the tiles that the other warp finishes (this one: part, part + 2)
         const uint32_t turn = meet + (c & 1) * (2 * DS * 8 * 512);
+        const uint32_t mine = turn + part * 8 * 512, other = turn + (part ^ 1) * 8 * 512;
+        auto give = [&](int i, const float (&v)[4]) {
+            tc::sts128(mine + i * 512, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        };
+        auto take = [&](int i, float (&v)[4]) {   // the sum of two is the same in either order
+            const uint4 o = tc::lds128(other + i * 512);
+            v[0] += __uint_as_float(o.x), v[1] += __uint_as_float(o.y), v[2] += __uint_as_float(o.z), v[3] += __uint_as_float(o.w);
+        };
+        float yq[2][4];
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
+        for (int n = 0; n < NC; n++) give(n, sk[n]);
 #pragma unroll
-            for (int e = 0; e < 4; e++) sk[n][e] *= down[e / 2], sq[n][e] *= down[e / 2];
-            tc::sts128(turn + (part * 8 + n) * 512, __float_as_uint(sk[n][0]), __float_as_uint(sk[n][1]), __float_as_uint(sk[n][2]), __float_as_uint(sk[n][3]));
-            tc::sts128(turn + (part * 8 + 4 + n) * 512, __float_as_uint(sq[n][0]), __float_as_uint(sq[n][1]), __float_as_uint(sq[n][2]), __float_as_uint(sq[n][3]));
-        }
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                yq[i][e] = part ? sq[2 * i + 1][e] : sq[2 * i][e];
+                sq[i][e] = part ? sq[2 * i][e] : sq[2 * i + 1][e];
+            }
+        give(4, sq[0]), give(5, sq[1]);
         bar_sync(kMeet + pair, 32 * DS);
-        // the keys' parts, in their order; then x in its place
-        float x[NT][4] = {};
 #pragma unroll
-        for (int r = 0; r < DS; r++)
+        for (int n = 0; n < NC; n++) take(n, sk[n]);
+        take(4, yq[0]), take(5, yq[1]);
+        // x in the place of S^T k
+        const T *vs = reinterpret_cast<const T *>(smem + slot * D::SLOT + D::V) + lane % 4 * D::TS + rd;   // TS bytes: 2 rows of TS / 2
+        float u[NC][4] = {};
+        {
+            uint32_t xp[3][NC / 2][4];
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-                const uint4 v = tc::lds128(turn + (r * 8 + n) * 512);
-                x[n][0] += __uint_as_float(v.x), x[n][1] += __uint_as_float(v.y), x[n][2] += __uint_as_float(v.z), x[n][3] += __uint_as_float(v.w);
-            }
-        const T *vs = reinterpret_cast<const T *>(smem + slot * D::SLOT + D::V);
+            for (int n = 0; n < NC; n++) {
+                const float4 w = *reinterpret_cast<const float4 *>(f + kXy * C + 2 * (n * 8 + lane % 4 * 2));   // B, .. of two rows
 #pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int i = n * 8 + lane % 4 * 2 + e % 2;
-                x[n][e] = fmaf(-f[kBetaReach * C + i], x[n][e], f[kBeta * C + i] * Storage<T>::to_f(vs[i * (D::VS / 2) + rd + e / 2 * 8]));
-            }
-        as_factor(x, hi, lo, down);
-        bar_sync(kInv + slot, STATE + 32);
-        float u[NT][4] = {};
-#pragma unroll
-        for (int n = 0; n < NT; n++) {   // rows n * 8 .. of T reach columns 0 .. n * 8 + 7
-            uint32_t b[4], l[4];
-            const uint32_t p = at + D::THI + (n * 8 + lane % 8) * D::TS + lane / 8 * 16;
-            ldsm4(b, p);
-            ldsm4(l, p + D::TLO - D::THI);
-#pragma unroll
-            for (int kk = 0; kk <= n / 2; kk++) {
-                mma_half(u[n], hi[kk], b[2 * kk], b[2 * kk + 1]);
-                mma_half(u[n], lo[kk], b[2 * kk], b[2 * kk + 1]);
-                mma_half(u[n], hi[kk], l[2 * kk], l[2 * kk + 1]);
-            }
-        }
-        float W[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int i = n * 8 + lane % 4 * 2 + e % 2;
-                u[n][e] *= down[e / 2] * f[kTDown * C + i];
-                W[n][e] = u[n][e] * f[kToEnd * C + i];
-            }
-        // the states after the chunk
-        as_factor(W, hi, lo, down);
-        const float total = f[kTotal * C];
-        float dS[NT][4] = {};
-#pragma unroll
-        for (int kk = 0; kk < 2; kk++)
-#pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t b[4];
-                ldsm4t(b, at + (kk * 16 + lane / 8 % 2 * 8 + lane % 8) * D::KS + (k0 + (n + lane / 16) * 8) * 2);
-                mma_half(dS[n], hi[kk], b[0], b[1]);
-                mma_half(dS[n + 1], hi[kk], b[2], b[3]);
-                mma_half(dS[n], lo[kk], b[0], b[1]);
-                mma_half(dS[n + 1], lo[kk], b[2], b[3]);
-            }
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) S[n][e] = fmaf(dS[n][e], down[e / 2], S[n][e] * total);
-        // y: this warp's share of the rows, tiles part, part + DS, ..
-        as_factor(u, hi, lo, down);
-#pragma unroll
-        for (int n = 0; n < NT; n++) {
-            if (n % DS != part) continue;
-            float o[4] = {}, w[4] = {};
-#pragma unroll
-            for (int r = 0; r < DS; r++) {
-                const uint4 v = tc::lds128(turn + (r * 8 + 4 + n) * 512);
-                o[0] += __uint_as_float(v.x), o[1] += __uint_as_float(v.y), o[2] += __uint_as_float(v.z), o[3] += __uint_as_float(v.w);
-            }
-            uint32_t b[4], l[4];
-            const uint32_t p = at + D::PHI + (n * 8 + lane % 8) * D::TS + lane / 8 * 16;
-            ldsm4(b, p);
-            if (FINE) ldsm4(l, p + D::PLO - D::PHI);
-#pragma unroll
-            for (int kk = 0; kk <= n / 2; kk++) {
-                mma_half(w, hi[kk], b[2 * kk], b[2 * kk + 1]);
-                if (FINE) {
-                    mma_half(w, lo[kk], b[2 * kk], b[2 * kk + 1]);
-                    mma_half(w, hi[kk], l[2 * kk], l[2 * kk + 1]);
+                for (int e = 0; e < 4; e++) {
+                    const float v = Storage<T>::to_f(vs[(n * 8 + e % 2) * (D::TS / 2) + e / 2 * 8]);
+                    sk[n][e] = fmaf(e % 2 ? -w.w : -w.y, sk[n][e], (e % 2 ? w.z : w.x) * v);
                 }
             }
+            as_bf16<3>(sk, xp);
+            bar_sync(kInv + slot, STATE + 32);
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int i = n * 8 + lane % 4 * 2 + e % 2, d = rd + e / 2 * 8;
-                const float v = fmaf(w[e], down[e / 2] * f[kPDown * C + i], o[e] * f[kQReach * C + i]);
-                if (c * C + i < len && d0 + d < a.dv) y[(t0 + c * C + i) * a.ld_y + d] = Storage<T>::from_f(v);
+            for (int n = 0; n < NC; n++) {   // rows n * 8 .. of T reach columns 0 .. n * 8 + 7
+                uint32_t b[3][4];
+                const uint32_t p = at + D::TP + (n * 8 + lane % 8) * D::TS + lane / 8 * 16;
+#pragma unroll
+                for (int m = 0; m < 3; m++) ldsm4(b[m], p + m * C * D::TS);
+#pragma unroll
+                for (int kk = 0; kk <= n / 2; kk++)
+#pragma unroll
+                    for (int m = 0; m < 3; m++)
+#pragma unroll
+                        for (int l = 0; l < 3 - m; l++) mma16<B>(u[n], xp[l][kk], b[m][2 * kk], b[m][2 * kk + 1]);
+            }
+        }
+        // the states after the chunk
+        const float total = f[kTotal * C];
+        {
+            uint32_t wp[3][NC / 2][4];
+            float W[NC][4], down[2];
+#pragma unroll
+            for (int n = 0; n < NC; n++) {
+                const float2 w = *reinterpret_cast<const float2 *>(f + kToEnd * C + n * 8 + lane % 4 * 2);
+#pragma unroll
+                for (int e = 0; e < 4; e++) W[n][e] = u[n][e] * (e % 2 ? w.y : w.x);
+            }
+            if constexpr (HALF) as_half(W, wp, down);
+            else as_bf16<3>(W, wp);
+#pragma unroll
+            for (int n = 0; n < NS; n += 2) {
+                float s0[4] = {}, s1[4] = {};
+                if (!HALF)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) s0[e] = S[n][e] * total, s1[e] = S[n + 1][e] * total;
+#pragma unroll
+                for (int kk = 0; kk < NC / 2; kk++) {
+                    uint32_t b[4];
+                    ldsm4t(b, at + (kk * 16 + lane / 8 % 2 * 8 + lane % 8) * D::KS + (k0 + (n + lane / 16) * 8) * 2);
+#pragma unroll
+                    for (int m = 0; m < (HALF ? 2 : 3); m++) {
+                        mma16<T>(s0, wp[m][kk], b[0], b[1]);
+                        mma16<T>(s1, wp[m][kk], b[2], b[3]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    S[n][e] = HALF ? fmaf(s0[e], down[e / 2], S[n][e] * total) : s0[e];
+                    S[n + 1][e] = HALF ? fmaf(s1[e], down[e / 2], S[n + 1][e] * total) : s1[e];
+                }
+            }
+        }
+        // y of this warp's tiles of rows
+        {
+            uint32_t up[3][NC / 2][4];
+            as_bf16<2>(u, up);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const int n = 2 * i + part;
+                float w[4] = {};
+                uint32_t b[2][4];
+                const uint32_t p = at + D::PP + (n * 8 + lane % 8) * D::TS + lane / 8 * 16;
+                ldsm4(b[0], p);
+                ldsm4(b[1], p + C * D::TS);
+#pragma unroll
+                for (int kk = 0; kk <= i; kk++) {
+                    mma16<B>(w, up[0][kk], b[0][2 * kk], b[0][2 * kk + 1]);
+                    mma16<B>(w, up[0][kk], b[1][2 * kk], b[1][2 * kk + 1]);
+                    mma16<B>(w, up[1][kk], b[0][2 * kk], b[0][2 * kk + 1]);
+                }
+                const int r = n * 8 + lane % 4 * 2, live = len - c * C - r;   // rows r and r + 1
+                const float2 reach = *reinterpret_cast<const float2 *>(f + kQReach * C + r);
+                T *to = y + (t0 + c * C + r) * a.ld_y;
+                if (live > 0 && in0) to[0] = Storage<T>::from_f(fmaf(yq[i][0], reach.x, w[0]));
+                if (live > 0 && in1) to[8] = Storage<T>::from_f(fmaf(yq[i][2], reach.x, w[2]));
+                to += a.ld_y;
+                if (live > 1 && in0) to[0] = Storage<T>::from_f(fmaf(yq[i][1], reach.y, w[1]));
+                if (live > 1 && in1) to[8] = Storage<T>::from_f(fmaf(yq[i][3], reach.y, w[3]));
             }
         }
         if (c + D::SLOTS < chunks) bar_arrive(kFree + slot, STATE + FRONT);
     }
     if (a.state_out && row >= 0) {
 #pragma unroll
-        for (int n = 0; n < NT; n++)
+        for (int n = 0; n < NS; n++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 const int k = k0 + n * 8 + lane % 4 * 2 + e % 2, d = rd + e / 2 * 8;

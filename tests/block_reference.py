@@ -17,7 +17,8 @@ def gated_delta(q, k, v, dt, a, b, dt_bias, softplus, sigmoid, normalize, scale,
     64 terms, the products that make them (a chunk's inverse, decays, norms), and factors kept in two 16-bit parts,
     2^-17 = 128 U.  e^G carries |G| times 12 U (softplus, product, sums of up to 64) and 4 U of its own.  In a chunk y
     is the sum of q.S, of the state before it, and of products with its rows' u, whose decayed sum `told` bounds;
-    for bf16 their factors may be kept in one f16 part: 2^-11 of the first's terms, and twice that of the others'."""
+    for 16-bit types both have factors of two bf16 parts, cut: 2^-16 of the first's terms, and for both factors and their
+    product of second parts three times that of the others'."""
     tokens, hk, dk = q.shape
     heads, dv = v.shape[1:]
     per, c = heads // hk, U * (dk + 256)
@@ -52,7 +53,7 @@ def gated_delta(q, k, v, dt, a, b, dt_bias, softplus, sigmoid, normalize, scale,
             told = decay * told + nk * np.abs(u)
             size = np.sqrt((S * S).sum(1))
             y[t] = np.einsum("hk,hkv->hv", qq, S)
-            part = 2.0 ** -11 * (size + 3.0 * told) if dtype == "bf16" else 0.0   # |S before| <= |S| + told
+            part = 2.0 ** -16 * (size + 4.0 * told) if dtype != "f32" else 0.0   # |S before| <= |S| + told
             e[t] = stored(y[t], nq * (err + c * size + c * nk * np.abs(u) + part), dtype)
         if kept:
             state[row] = S
