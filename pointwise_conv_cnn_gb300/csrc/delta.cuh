@@ -28,7 +28,7 @@ struct DeltaArgs {
 // G of one row and head, and its step B.  A scalar a row: the library's functions, whose errors are units of
 // the last place.
 __device__ __forceinline__ float log_decay(float v, float a, int softplus) {
-    if (softplus) v = v > 0.0f ? v + log1pf(expf(-v)) : log1pf(expf(v));
+    if (softplus) v = (v < 0.0f ? 0.0f : v) + log1pf(expf(-fabsf(v)));
     return v * a;
 }
 __device__ __forceinline__ float step_of(float v, int sigmoid) { return sigmoid ? 1.0f / (1.0f + expf(-v)) : v; }

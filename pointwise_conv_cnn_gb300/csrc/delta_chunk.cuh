@@ -17,7 +17,7 @@ template <int DK> struct DeltaChunk {
     static constexpr int C = 32;                      // rows of a chunk
     static constexpr int DS = 2, KW = DK / DS;        // warps that share 16 columns' states, keys of each
     static constexpr int STATE = 2 * DS, FRONT = 4;   // warps
-    static constexpr int THREADS = 32 * (STATE + FRONT + 1);
+    static constexpr int THREADS = 32 * (STATE + FRONT + 2);
     static constexpr int SLOTS = 3;
     static constexpr int KS = 2 * DK + 16;            // bytes of a row of keys: eight rows in different banks
     static constexpr int TS = 80;                     // of T's and the rows' products' 16-bit parts, and of values
@@ -151,8 +151,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
     using B = __nv_bfloat16;
     constexpr int C = D::C, DS = D::DS, NS = D::KW / 8, NC = C / 8;   // tiles of 8 keys of a warp, of 8 rows of a chunk
     constexpr bool HALF = std::is_same<T, __half>::value;
-    constexpr int kFull = 1, kInv = 4, kFree = 7, kMeet = 10, kTeam = 12;   // barriers; the first three by slot
-    constexpr int ALL = D::THREADS, STATE = 32 * D::STATE, FRONT = 32 * D::FRONT;
+    constexpr int kFull = 1, kInv = 4, kFree = 7, kRows = 10, kMeet = 13, kTeam = 15;   // barriers; the first four by slot
+    constexpr int ALL = D::THREADS - 32, STATE = 32 * D::STATE, FRONT = 32 * D::FRONT;
     extern __shared__ __align__(16) unsigned char smem[];
     const uint32_t base = tc::smem_u32(smem);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -173,8 +173,6 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
         const T *kp = static_cast<const T *>(a.kp) + (size_t)g * a.dk, *qp = static_cast<const T *>(a.qp) + (size_t)g * a.dk;
         const T *vp = static_cast<const T *>(a.vp) + (size_t)h * a.dv + d0;
         const int vcols = min(a.dv - d0, kDeltaCols), vc = tid % 4 * 8;
-        const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-        float dt = 0.0f, bv = 0.0f;
         auto load = [&](int c) {
             const uint32_t to = base + c % D::SLOTS * D::SLOT;
             unsigned char *plain = smem + c % D::SLOTS * D::SLOT;
@@ -200,42 +198,19 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             else *reinterpret_cast<uint4 *>(plain + at) = load_keys(v, vc, vcols, live, false);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto load_scalars = [&](int c) {
-            const bool live = c * C + lane < len;
-            dt = live ? Storage<T>::to_f(static_cast<const T *>(a.dt)[(t0 + c * C + lane) * a.ld_dt + h]) : 0.0f;
-            bv = live ? Storage<T>::to_f(static_cast<const T *>(a.b)[(t0 + c * C + lane) * a.ld_b + h]) : 0.0f;
-        };
-        if (chunks) {
-            load(0);
-            if (w == 0) load_scalars(0);
-        }
+        if (chunks) load(0);
         for (int c = 0; c < chunks; c++) {
             const int slot = c % D::SLOTS;
             unsigned char *at = smem + slot * D::SLOT;
             float *f = factors(slot);
             if (c + 1 < chunks) {
-                if (c + 1 >= D::SLOTS) bar_sync(kFree + (c + 1) % D::SLOTS, STATE + FRONT);
+                if (c + 1 >= D::SLOTS) bar_sync(kFree + (c + 1) % D::SLOTS, STATE + FRONT + 32);
                 load(c + 1);
             } else {
                 asm volatile("cp.async.commit_group;" ::: "memory");
             }
-            if (w == 0) {
-                const bool live = c * C + lane < len;
-                float G = log_decay(dt + bias, av, a.softplus);
-                G = !live ? 0.0f : G < -1000.0f ? -1000.0f : G;   // nothing is left below -104, and sums stay numbers
-                double sum = G;
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const double before = __shfl_up_sync(~0u, sum, m);
-                    if (lane >= m) sum += before;
-                }
-                const float hi = (float)sum;
-                f[kSumHi * C + lane] = hi, f[kSumLo * C + lane] = (float)(sum - hi);
-                f[kBeta * C + lane] = live ? step_of(bv, a.sigmoid) : 0.0f;
-                if (c + 1 < chunks) load_scalars(c + 1);
-            }
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            bar_sync(kTeam, FRONT);
+            bar_sync(kRows + slot, FRONT + 32);
             // products of keys (warps 0, 2) and of queries with keys (1, 3): rows 16 .. 31 (0, 1), 0 .. 15 (2, 3); and of
             // those rows with themselves
             const int m0 = w < 2 ? 16 : 0;
@@ -311,6 +286,31 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
         }
         return;
     }
+    if (warp == D::STATE + D::FRONT + 1) {
+        // ---- the rows' decays and steps, a row a lane
+        const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+        for (int c = 0; c < chunks; c++) {
+            const int slot = c % D::SLOTS;
+            const bool live = c * C + lane < len;
+            const long long t = live ? t0 + c * C + lane : t0;
+            const float dt = Storage<T>::to_f(static_cast<const T *>(a.dt)[t * a.ld_dt + h]);
+            const float bv = Storage<T>::to_f(static_cast<const T *>(a.b)[t * a.ld_b + h]);
+            float G = log_decay(dt + bias, av, a.softplus);
+            G = !live ? 0.0f : G < -1000.0f ? -1000.0f : G;   // nothing is left below -104, and sums stay numbers
+            double sum = G;   // differences of these sums keep a float's precision where they are small
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double before = __shfl_up_sync(~0u, sum, m);
+                if (lane >= m) sum += before;
+            }
+            const float hi = (float)sum, beta = live ? step_of(bv, a.sigmoid) : 0.0f;
+            if (c >= D::SLOTS) bar_sync(kFree + slot, STATE + FRONT + 32);
+            float *f = factors(slot);
+            f[kSumHi * C + lane] = hi, f[kSumLo * C + lane] = (float)(sum - hi), f[kBeta * C + lane] = beta;
+            bar_arrive(kRows + slot, FRONT + 32);
+        }
+        return;
+    }
     if (warp == D::STATE + D::FRONT) {
         // ---- the inverse.  A column of a diagonal block a lane: row i is that of 1 less the rows above it, by A.
         float *own = reinterpret_cast<float *>(smem + D::SLOTS * D::SLOT + D::XCH);
@@ -319,13 +319,13 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             const int slot = c % D::SLOTS;
             bar_sync(kFull + slot, ALL);
             const float *A = reinterpret_cast<const float *>(smem + slot * D::SLOT + D::A);
-            unsigned char *to = smem + slot * D::SLOT + D::TP;
+            unsigned short *to = reinterpret_cast<unsigned short *>(smem + slot * D::SLOT + D::TP);
             auto put = [&](int i, int col, float v) {   // in three parts
 #pragma unroll
                 for (int m = 0; m < 3; m++) {
-                    const uint32_t x = __float_as_uint(v);
-                    *reinterpret_cast<unsigned short *>(to + m * C * D::TS + i * D::TS + col * 2) = (unsigned short)(x >> 16);
-                    v -= __uint_as_float(x & 0xFFFF0000u);
+                    const uint32_t b = __float_as_uint(v);
+                    to[m * C * (D::TS / 2) + i * (D::TS / 2) + col] = (unsigned short)(b >> 16);
+                    v -= __uint_as_float(b & 0xFFFF0000u);
                 }
             };
             float t[16];
@@ -342,40 +342,40 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                         if (m + k < i) s[k & 1] = fmaf(-e[k], t[m + k], s[k & 1]);
                 }
                 t[i] = s[0] + s[1];
-                own[(16 * half + i) * D::AS + j] = t[i];
-                put(16 * half + i, 16 * half + j, t[i]);
+                own[(16 * half + i) * D::AS + 16 * half + j] = t[i];
             }
             __syncwarp();
-            // below them: -T22 (A21 T11), eight rows a half of the lanes
-            float x[16];
+            // Below them -T22 A21 T11, as the transposed products T11^T A21^T and that times T22^T, whose right factors lie
+            // as they are needed and whose sums are the next left factors.
+            float m1[2][4], m2[2][4] = {};
+            uint32_t left[3][1][4];
+            auto times = [&](const float *from, float (&sum)[2][4]) {   // left factors by the rows of `from`
 #pragma unroll
-            for (int m = 0; m < 16; m++) x[m] = own[m * D::AS + j];
-            float p[16];
-            auto rows = [&](const float *from, float (&out)[8]) {
+                for (int n = 0; n < 2; n++) {
+                    const float *p = from + (n * 8 + lane / 4) * D::AS + lane % 4 * 2;
+                    float2 lo = *reinterpret_cast<const float2 *>(p), hi = *reinterpret_cast<const float2 *>(p + 8);
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    float s[2] = {};
+                    for (int m = 0; m < 3; m++) {
+                        uint32_t b0, b1;
+                        cut(lo.x, lo.y, b0), cut(hi.x, hi.y, b1);
 #pragma unroll
-                    for (int m = 0; m < 16; m += 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(from + (8 * half + i) * D::AS + m);
-                        s[0] = fmaf(v.x, x[m], s[0]), s[1] = fmaf(v.y, x[m + 1], s[1]);
-                        s[0] = fmaf(v.z, x[m + 2], s[0]), s[1] = fmaf(v.w, x[m + 3], s[1]);
+                        for (int l = 0; l < 3 - m; l++) mma16<B>(sum[n], left[l][0], b0, b1);
                     }
-                    out[i] = s[0] + s[1];
                 }
             };
-            float r[8];
-            rows(A + 16 * D::AS, r);
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const float other = __shfl_xor_sync(~0u, r[i], 16);
-                p[i] = half ? other : r[i], p[8 + i] = half ? r[i] : other;
-            }
+            for (int e = 0; e < 8; e++)   // tile e / 4 of the left factor: inner places (rows of T11) 8 (e / 4) ..
+                m2[e / 4][e % 4] = own[(lane % 4 * 2 + e % 2 + e / 4 * 8) * D::AS + lane / 4 + e / 2 % 2 * 8];
+            as_bf16<3>(m2, left);
 #pragma unroll
-            for (int m = 0; m < 16; m++) x[m] = p[m];
-            rows(own + 16 * D::AS, r);
+            for (int e = 0; e < 8; e++) m1[e / 4][e % 4] = m2[e / 4][e % 4] = 0.0f;
+            times(A + 16 * D::AS, m1);
+            as_bf16<3>(m1, left);
+            times(own + 16 * (D::AS + 1), m2);
 #pragma unroll
-            for (int i = 0; i < 8; i++) put(16 + 8 * half + i, j, -r[i]);
+            for (int i = 0; i < 16; i++) put(16 * half + i, 16 * half + j, t[i]);
+#pragma unroll
+            for (int e = 0; e < 8; e++) put(16 + e / 4 * 8 + lane % 4 * 2 + e % 2, lane / 4 + e / 2 % 2 * 8, -m2[e / 4][e % 4]);
             __syncwarp();
             bar_arrive(kInv + slot, STATE + 32);
         }
@@ -552,7 +552,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 if (live > 1 && in1) to[8] = Storage<T>::from_f(fmaf(yq[i][3], reach.y, w[3]));
             }
         }
-        if (c + D::SLOTS < chunks) bar_arrive(kFree + slot, STATE + FRONT);
+        if (c + D::SLOTS < chunks) bar_arrive(kFree + slot, STATE + FRONT + 32);
     }
     if (a.state_out && row >= 0) {
 #pragma unroll
