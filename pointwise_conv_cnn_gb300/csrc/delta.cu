@@ -126,7 +126,11 @@ __global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const D
                                     f.w * fmaf(qk, u[2], f.x * sq.z), f.w * fmaf(qk, u[3], f.x * sq.w)};
                 T *to = y + (t + j) * a.ld_y;
                 if (VEC) {
-                    if (d < a.dv) reinterpret_cast<Vec<T, 4> *>(to)->put(o);
+                    if (d < a.dv) {
+                        Vec<T, 4> v4;
+                        v4.put(o);
+                        *reinterpret_cast<Vec<T, 4> *>(to) = v4;
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; e++)
