@@ -18,7 +18,7 @@ template <int DK> struct DeltaChunk {
     static constexpr int DS = 2, KW = DK / DS;        // warps that share 16 columns' states, keys of each
     static constexpr int STATE = 2 * DS, FRONT = 4;   // warps
     static constexpr int THREADS = 32 * (STATE + FRONT + 2);
-    static constexpr int SLOTS = 3;
+    static constexpr int SLOTS = 4, AHEAD = 2;        // chunks in flight, chunks whose rows are asked for ahead
     static constexpr int KS = 2 * DK + 16;            // bytes of a row of keys: eight rows in different banks
     static constexpr int TS = 80;                     // of T's and the rows' products' 16-bit parts, and of values
     static constexpr int AS = 36;                     // floats of a row of A, and of T on its way
@@ -28,6 +28,7 @@ template <int DK> struct DeltaChunk {
     static constexpr int XCH = 2 * 2 * DS * 8 * 512;   // sums on their way between warps: [turn][16 columns][warp][16 bytes][lane]
     static constexpr int TMP = C * AS * 4;             // T's diagonal blocks
     static constexpr int SMEM = SLOTS * SLOT + XCH + TMP;
+    static_assert(AHEAD >= 2 && SLOTS > AHEAD, "a slot is waited for before its rows' factors are made");
 };
 // A slot's factors by row: B and B e^c / |k| (for x), e^c / |q| scale (y), e^(c_last - c) / |k| (the states).
 enum { kXy = 0 /* two a row */, kQReach = 2, kToEnd, kSumHi, kSumLo, kBeta, kTotal };
@@ -151,7 +152,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
     using B = __nv_bfloat16;
     constexpr int C = D::C, DS = D::DS, NS = D::KW / 8, NC = C / 8;   // tiles of 8 keys of a warp, of 8 rows of a chunk
     constexpr bool HALF = std::is_same<T, __half>::value;
-    constexpr int kFull = 1, kInv = 4, kFree = 7, kRows = 10, kMeet = 13, kTeam = 15;   // barriers; the first four by slot
+    constexpr int kFull = 0, kInv = 4, kFree = 8, kMeet = 12, kTeam = 14, kRows = 15;   // barriers; the first three by slot
     constexpr int ALL = D::THREADS - 32, STATE = 32 * D::STATE, FRONT = 32 * D::FRONT;
     extern __shared__ __align__(16) unsigned char smem[];
     const uint32_t base = tc::smem_u32(smem);
@@ -173,47 +174,52 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
         const T *kp = static_cast<const T *>(a.kp) + (size_t)g * a.dk, *qp = static_cast<const T *>(a.qp) + (size_t)g * a.dk;
         const T *vp = static_cast<const T *>(a.vp) + (size_t)h * a.dv + d0;
         const int vcols = min(a.dv - d0, kDeltaCols), vc = tid % 4 * 8;
+        // A thread's pieces of the rows to come: where they are, and how far the next chunk's.
+        const T *k_at = kp + (t0 + r0) * a.ld_k + (col < a.dk ? col : 0), *q_at = qp + (t0 + r0) * a.ld_q + (col < a.dk ? col : 0);
+        const T *v_at = vp + (t0 + tid / 4) * a.ld_v + (vc < vcols ? vc : 0);
+        const long long k_row = RPP * a.ld_k, q_row = RPP * a.ld_q;
         auto load = [&](int c) {
-            const uint32_t to = base + c % D::SLOTS * D::SLOT;
-            unsigned char *plain = smem + c % D::SLOTS * D::SLOT;
+            const int slot = c % D::SLOTS;
+            const uint32_t to = base + slot * D::SLOT + r0 * D::KS + col * 2, to_v = base + slot * D::SLOT + D::V + tid / 4 * D::TS + vc * 2;
+            unsigned char *plain = smem + (to - base);
+            const int left = len - c * C - r0;   // rows of this thread's, RPP apart
+            const T *k = k_at, *q = q_at;
 #pragma unroll
             for (int p = 0; p < PASS; p++) {
-                const int row = r0 + p * RPP;
-                const bool live = c * C + row < len;
-                const long long t = live ? t0 + c * C + row : t0;
-                const int at = row * D::KS + col * 2;
+                const bool live = p * RPP < left;
                 if (a.vec) {
-                    const int e = col < a.dk ? col : 0;
-                    copy16(to + at, kp + t * a.ld_k + e, live && col < a.dk);
-                    copy16(to + D::Q + at, qp + t * a.ld_q + e, live && col < a.dk);
+                    copy16(to + p * RPP * D::KS, live ? k : kp, live && col < a.dk);
+                    copy16(to + D::Q + p * RPP * D::KS, live ? q : qp, live && col < a.dk);
                 } else {
-                    *reinterpret_cast<uint4 *>(plain + at) = load_keys(kp + t * a.ld_k, col, a.dk, live, false);
-                    *reinterpret_cast<uint4 *>(plain + D::Q + at) = load_keys(qp + t * a.ld_q, col, a.dk, live, false);
+                    *reinterpret_cast<uint4 *>(plain + p * RPP * D::KS) = load_keys(k - (col < a.dk ? col : 0), col, a.dk, live, false);
+                    *reinterpret_cast<uint4 *>(plain + D::Q + p * RPP * D::KS) = load_keys(q - (col < a.dk ? col : 0), col, a.dk, live, false);
                 }
+                k += k_row, q += q_row;
             }
+            k_at = k, q_at = q;   // PASS * RPP rows are a chunk
             const bool live = c * C + tid / 4 < len;
-            const T *v = vp + (live ? t0 + c * C + tid / 4 : t0) * a.ld_v;
-            const int at = D::V + tid / 4 * D::TS + vc * 2;
-            if (a.vec_v) copy16(to + at, v + (vc < vcols ? vc : 0), live && vc < vcols);
-            else *reinterpret_cast<uint4 *>(plain + at) = load_keys(v, vc, vcols, live, false);
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (a.vec_v) copy16(to_v, live ? v_at : vp, live && vc < vcols);
+            else *reinterpret_cast<uint4 *>(smem + (to_v - base)) = load_keys(v_at - (vc < vcols ? vc : 0), vc, vcols, live, false);
+            v_at += C * a.ld_v;
         };
-        if (chunks) load(0);
-        for (int c = 0; c < chunks; c++) {
+#pragma unroll 1
+        for (int c = -D::AHEAD; c < chunks; c++) {
+            const int ahead = c + D::AHEAD;
+            if (ahead < chunks) {
+                if (ahead >= D::SLOTS) bar_sync(kFree + ahead % D::SLOTS, STATE + FRONT);
+                load(ahead);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (c < 0) continue;
             const int slot = c % D::SLOTS;
             unsigned char *at = smem + slot * D::SLOT;
             float *f = factors(slot);
-            if (c + 1 < chunks) {
-                if (c + 1 >= D::SLOTS) bar_sync(kFree + (c + 1) % D::SLOTS, STATE + FRONT + 32);
-                load(c + 1);
-            } else {
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            }
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            bar_sync(kRows + slot, FRONT + 32);
-            // products of keys (warps 0, 2) and of queries with keys (1, 3): rows 16 .. 31 (0, 1), 0 .. 15 (2, 3); and of
-            // those rows with themselves
-            const int m0 = w < 2 ? 16 : 0;
+            asm volatile("cp.async.wait_group %0;" ::"n"(D::AHEAD) : "memory");
+            bar_sync(kRows, FRONT + 32);
+            // products of keys (warps 0, 2) and of queries with keys (1, 3): rows 0 .. 15 (0, 1: beside the two warps that
+            // follow these four on the SM's schedulers), 16 .. 31 (2, 3), whose are twice as many; and of those rows with
+            // themselves
+            const int m0 = w < 2 ? 0 : 16;
             const bool queries = w & 1;
             const uint32_t ka = base + slot * D::SLOT, qa = ka + (queries ? D::Q : 0);
             float s[4][4] = {}, own[2][4] = {};
@@ -274,7 +280,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 }
             }
             bar_sync(kTeam, FRONT);   // all have read the rows' lengths, which become the rows' factors
-            if (w == 2) {
+            if (w == 1) {
                 const float hi = f[kSumHi * C + lane], lo = f[kSumLo * C + lane], beta = f[kBeta * C + lane];
                 const float reach = ex2(kLog2e * hi) * (1.0f + lo), fk = f[kToEnd * C + lane];
                 *reinterpret_cast<float2 *>(f + kXy * C + 2 * lane) = make_float2(beta, beta * reach * fk);
@@ -289,12 +295,16 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
     if (warp == D::STATE + D::FRONT + 1) {
         // ---- the rows' decays and steps, a row a lane
         const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+        auto fetch = [&](const void *p, long long ld, int c) {
+            const long long t = c * C + lane < len ? t0 + c * C + lane : t0;
+            return Storage<T>::to_f(static_cast<const T *>(p)[t * ld + h]);
+        };
+        float dt_next = chunks ? fetch(a.dt, a.ld_dt, 0) : 0.0f, b_next = chunks ? fetch(a.b, a.ld_b, 0) : 0.0f;
         for (int c = 0; c < chunks; c++) {
             const int slot = c % D::SLOTS;
             const bool live = c * C + lane < len;
-            const long long t = live ? t0 + c * C + lane : t0;
-            const float dt = Storage<T>::to_f(static_cast<const T *>(a.dt)[t * a.ld_dt + h]);
-            const float bv = Storage<T>::to_f(static_cast<const T *>(a.b)[t * a.ld_b + h]);
+            const float dt = dt_next, bv = b_next;
+            if (c + 1 < chunks) dt_next = fetch(a.dt, a.ld_dt, c + 1), b_next = fetch(a.b, a.ld_b, c + 1);
             float G = log_decay(dt + bias, av, a.softplus);
             G = !live ? 0.0f : G < -1000.0f ? -1000.0f : G;   // nothing is left below -104, and sums stay numbers
             double sum = G;   // differences of these sums keep a float's precision where they are small
@@ -304,10 +314,10 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 if (lane >= m) sum += before;
             }
             const float hi = (float)sum, beta = live ? step_of(bv, a.sigmoid) : 0.0f;
-            if (c >= D::SLOTS) bar_sync(kFree + slot, STATE + FRONT + 32);
+            // the slot is free: the four warps have met this one for the chunk before, and waited for it earlier still
             float *f = factors(slot);
             f[kSumHi * C + lane] = hi, f[kSumLo * C + lane] = (float)(sum - hi), f[kBeta * C + lane] = beta;
-            bar_arrive(kRows + slot, FRONT + 32);
+            bar_sync(kRows, FRONT + 32);
         }
         return;
     }
@@ -408,25 +418,25 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             if constexpr (HALF) as_half(S, sp, down);
             else as_bf16<3>(S, sp);
             bar_sync(kFull + slot, ALL);
+            // Every sum of products goes round its tiles, so that one product does not wait for the one before: a product's
+            // sum is there after 21 cycles, and the next may begin after 8.
+            const uint32_t keys = at + (lane / 16 * 8 + lane % 8) * D::KS + (k0 + lane / 8 % 2 * 8) * 2;
 #pragma unroll
-            for (int kk = 0; kk < NS / 2; kk++)
+            for (int kk = 0; kk < NS / 2; kk++) {
+                uint32_t b[2][4];
 #pragma unroll
-                for (int n = 0; n < NC; n += 2) {
-                    uint32_t b[4];
-                    const uint32_t p = at + (n * 8 + lane / 16 * 8 + lane % 8) * D::KS + (k0 + kk * 16 + lane / 8 % 2 * 8) * 2;
-                    ldsm4(b, p);
+                for (int i = 0; i < 2; i++) ldsm4(b[i], keys + i * 16 * D::KS + kk * 32);
 #pragma unroll
-                    for (int m = 0; m < (HALF ? 2 : 3); m++) {
-                        mma16<T>(sk[n], sp[m][kk], b[0], b[1]);
-                        mma16<T>(sk[n + 1], sp[m][kk], b[2], b[3]);
-                    }
-                    ldsm4(b, p + D::Q);
+                for (int m = 0; m < (HALF ? 2 : 3); m++)
 #pragma unroll
-                    for (int m = 0; m < 2; m++) {
-                        mma16<T>(sq[n], sp[m][kk], b[0], b[1]);
-                        mma16<T>(sq[n + 1], sp[m][kk], b[2], b[3]);
-                    }
-                }
+                    for (int n = 0; n < NC; n++) mma16<T>(sk[n], sp[m][kk], b[n / 2][n % 2 * 2], b[n / 2][n % 2 * 2 + 1]);
+#pragma unroll
+                for (int i = 0; i < 2; i++) ldsm4(b[i], keys + D::Q + i * 16 * D::KS + kk * 32);
+#pragma unroll
+                for (int m = 0; m < 2; m++)
+#pragma unroll
+                    for (int n = 0; n < NC; n++) mma16<T>(sq[n], sp[m][kk], b[n / 2][n % 2 * 2], b[n / 2][n % 2 * 2 + 1]);
+            }
             if (HALF)
 #pragma unroll
                 for (int n = 0; n < NC; n++)
@@ -475,17 +485,16 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             as_bf16<3>(sk, xp);
             bar_sync(kInv + slot, STATE + 32);
 #pragma unroll
-            for (int n = 0; n < NC; n++) {   // rows n * 8 .. of T reach columns 0 .. n * 8 + 7
-                uint32_t b[3][4];
-                const uint32_t p = at + D::TP + (n * 8 + lane % 8) * D::TS + lane / 8 * 16;
+            for (int m = 0; m < 3; m++) {   // rows n * 8 .. of T reach columns 0 .. n * 8 + 7
+                uint32_t b[NC][4];
 #pragma unroll
-                for (int m = 0; m < 3; m++) ldsm4(b[m], p + m * C * D::TS);
+                for (int n = 0; n < NC; n++) ldsm4(b[n], at + D::TP + m * C * D::TS + (n * 8 + lane % 8) * D::TS + lane / 8 * 16);
 #pragma unroll
-                for (int kk = 0; kk <= n / 2; kk++)
+                for (int l = 0; l < 3 - m; l++)
 #pragma unroll
-                    for (int m = 0; m < 3; m++)
+                    for (int kk = 0; kk < NC / 2; kk++)
 #pragma unroll
-                        for (int l = 0; l < 3 - m; l++) mma16<B>(u[n], xp[l][kk], b[m][2 * kk], b[m][2 * kk + 1]);
+                        for (int n = 2 * kk; n < NC; n++) mma16<B>(u[n], xp[l][kk], b[n][2 * kk], b[n][2 * kk + 1]);
             }
         }
         // the states after the chunk
@@ -501,28 +510,29 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             }
             if constexpr (HALF) as_half(W, wp, down);
             else as_bf16<3>(W, wp);
+            float add[NS][4];
 #pragma unroll
-            for (int n = 0; n < NS; n += 2) {
-                float s0[4] = {}, s1[4] = {};
-                if (!HALF)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) s0[e] = S[n][e] * total, s1[e] = S[n + 1][e] * total;
-#pragma unroll
-                for (int kk = 0; kk < NC / 2; kk++) {
-                    uint32_t b[4];
-                    ldsm4t(b, at + (kk * 16 + lane / 8 % 2 * 8 + lane % 8) * D::KS + (k0 + (n + lane / 16) * 8) * 2);
-#pragma unroll
-                    for (int m = 0; m < (HALF ? 2 : 3); m++) {
-                        mma16<T>(s0, wp[m][kk], b[0], b[1]);
-                        mma16<T>(s1, wp[m][kk], b[2], b[3]);
-                    }
-                }
+            for (int n = 0; n < NS; n++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    S[n][e] = HALF ? fmaf(s0[e], down[e / 2], S[n][e] * total) : s0[e];
-                    S[n + 1][e] = HALF ? fmaf(s1[e], down[e / 2], S[n + 1][e] * total) : s1[e];
+                    S[n][e] *= total;
+                    add[n][e] = HALF ? 0.0f : S[n][e];
                 }
+#pragma unroll
+            for (int kk = 0; kk < NC / 2; kk++) {
+                uint32_t b[NS / 2][4];
+#pragma unroll
+                for (int i = 0; i < NS / 2; i++)
+                    ldsm4t(b[i], at + (kk * 16 + lane / 8 % 2 * 8 + lane % 8) * D::KS + (k0 + (2 * i + lane / 16) * 8) * 2);
+#pragma unroll
+                for (int m = 0; m < (HALF ? 2 : 3); m++)
+#pragma unroll
+                    for (int n = 0; n < NS; n++) mma16<T>(add[n], wp[m][kk], b[n / 2][n % 2 * 2], b[n / 2][n % 2 * 2 + 1]);
             }
+#pragma unroll
+            for (int n = 0; n < NS; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) S[n][e] = HALF ? fmaf(add[n][e], down[e / 2], S[n][e]) : add[n][e];
         }
         // y of this warp's tiles of rows
         {
@@ -552,7 +562,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 if (live > 1 && in1) to[8] = Storage<T>::from_f(fmaf(yq[i][3], reach.y, w[3]));
             }
         }
-        if (c + D::SLOTS < chunks) bar_arrive(kFree + slot, STATE + FRONT + 32);
+        if (c + D::SLOTS < chunks) bar_arrive(kFree + slot, STATE + FRONT);
     }
     if (a.state_out && row >= 0) {
 #pragma unroll
