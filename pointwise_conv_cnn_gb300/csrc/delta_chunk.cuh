@@ -23,7 +23,7 @@ template <int DK> struct DeltaChunk {
     static constexpr int TS = 80;                     // of T's and the rows' products' 16-bit parts, and of values
     static constexpr int AS = 36;                     // floats of a row of A, and of T on its way
     // a slot's parts, bytes
-    static constexpr int Q = C * KS, V = 2 * C * KS, TP = V + C * TS, PP = TP + 3 * C * TS, A = PP + 2 * C * TS,
+    static constexpr int Q = C * KS, V = 2 * C * KS, TP = V + C * TS, PP = TP + 2 * C * TS, A = PP + 2 * C * TS,
                          SC = A + C * AS * 4, SLOT = SC + 8 * C * 4;
     static constexpr int XCH = 2 * 2 * DS * 8 * 512;   // sums on their way between warps: [turn][16 columns][warp][16 bytes][lane]
     static constexpr int TMP = C * AS * 4;             // T's diagonal blocks
@@ -143,10 +143,10 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool live)
 // rows' lengths are the products of keys and of queries with themselves.  One inverts 1 + A: two blocks of 16 by forward
 // substitution, a column a lane, and the block below them by two products, in 32 bits.
 //
-// Rounding: keys and queries are used as they are, and their lengths, decays and steps applied to sums in 32 bits.  x, u
-// and T enter products in three bf16 parts, which hold all 24 bits, and so do S and the decayed u beside bf16 keys; beside
-// f16 keys they have two f16 parts, 22 bits.  Products of parts below 2^-23 are left out.  What only y needs (S^T q, P u)
-// has two parts, 2^-16 at least, where y keeps 2^-9 or 2^-12.
+// Rounding: keys and queries are used as they are, and their lengths, decays and steps applied to sums in 32 bits.  S and
+// the decayed u enter products with bf16 keys in three bf16 parts, which hold all 24 bits, and with f16 keys in two f16
+// parts, 22 bits, as x and T do; products of second f16 parts, below 2^-22, are left out.  What only y needs (S^T q, P u)
+// has two parts, 2^-16 at least, where y keeps 2^-8 or 2^-11.
 template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::THREADS, 1) delta_chunk_kernel(const DeltaArgs a) {
     using D = DeltaChunk<DK>;
     using B = __nv_bfloat16;
@@ -329,14 +329,11 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             const int slot = c % D::SLOTS;
             bar_sync(kFull + slot, ALL);
             const float *A = reinterpret_cast<const float *>(smem + slot * D::SLOT + D::A);
-            unsigned short *to = reinterpret_cast<unsigned short *>(smem + slot * D::SLOT + D::TP);
-            auto put = [&](int i, int col, float v) {   // in three parts
-#pragma unroll
-                for (int m = 0; m < 3; m++) {
-                    const uint32_t b = __float_as_uint(v);
-                    to[m * C * (D::TS / 2) + i * (D::TS / 2) + col] = (unsigned short)(b >> 16);
-                    v -= __uint_as_float(b & 0xFFFF0000u);
-                }
+            __half *to = reinterpret_cast<__half *>(smem + slot * D::SLOT + D::TP);
+            auto put = [&](int i, int col, float v) {   // in two parts
+                const __half hi = __float2half_rn(v);
+                to[i * (D::TS / 2) + col] = hi;
+                to[(C + i) * (D::TS / 2) + col] = __float2half_rn(v - __half2float(hi));
             };
             float t[16];
             const float *Ad = A + 16 * half * (D::AS + 1);
@@ -357,35 +354,42 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             __syncwarp();
             // Below them -T22 A21 T11, as the transposed products T11^T A21^T and that times T22^T, whose right factors lie
             // as they are needed and whose sums are the next left factors.
-            float m1[2][4], m2[2][4] = {};
-            uint32_t left[3][1][4];
-            auto times = [&](const float *from, float (&sum)[2][4]) {   // left factors by the rows of `from`
+            // None is scaled: a product over 65504 is no number any more (as the rule multiplies keys that are not
+            // normalised, within 32 rows).
+            float sum[2][4];
+            uint32_t left[2][4];
+            auto factor = [&] {
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    split2(sum[e / 2][e % 2 * 2], sum[e / 2][e % 2 * 2 + 1], left[0][e], left[1][e]);
+                }
+            };
+            auto times = [&](const float *from) {   // left factors by the rows of `from`
 #pragma unroll
                 for (int n = 0; n < 2; n++) {
                     const float *p = from + (n * 8 + lane / 4) * D::AS + lane % 4 * 2;
-                    float2 lo = *reinterpret_cast<const float2 *>(p), hi = *reinterpret_cast<const float2 *>(p + 8);
+                    const float2 lo = *reinterpret_cast<const float2 *>(p), hi = *reinterpret_cast<const float2 *>(p + 8);
+                    uint32_t b0[2], b1[2];
+                    split2(lo.x, lo.y, b0[0], b0[1]), split2(hi.x, hi.y, b1[0], b1[1]);
+                    float s[4] = {};
+                    mma16<__half>(s, left[0], b0[1], b1[1]);
+                    mma16<__half>(s, left[1], b0[0], b1[0]);
+                    mma16<__half>(s, left[0], b0[0], b1[0]);
 #pragma unroll
-                    for (int m = 0; m < 3; m++) {
-                        uint32_t b0, b1;
-                        cut(lo.x, lo.y, b0), cut(hi.x, hi.y, b1);
-#pragma unroll
-                        for (int l = 0; l < 3 - m; l++) mma16<B>(sum[n], left[l][0], b0, b1);
-                    }
+                    for (int e = 0; e < 4; e++) sum[n][e] = s[e];
                 }
             };
 #pragma unroll
             for (int e = 0; e < 8; e++)   // tile e / 4 of the left factor: inner places (rows of T11) 8 (e / 4) ..
-                m2[e / 4][e % 4] = own[(lane % 4 * 2 + e % 2 + e / 4 * 8) * D::AS + lane / 4 + e / 2 % 2 * 8];
-            as_bf16<3>(m2, left);
-#pragma unroll
-            for (int e = 0; e < 8; e++) m1[e / 4][e % 4] = m2[e / 4][e % 4] = 0.0f;
-            times(A + 16 * D::AS, m1);
-            as_bf16<3>(m1, left);
-            times(own + 16 * (D::AS + 1), m2);
+                sum[e / 4][e % 4] = own[(lane % 4 * 2 + e % 2 + e / 4 * 8) * D::AS + lane / 4 + e / 2 % 2 * 8];
+            factor();
+            times(A + 16 * D::AS);
+            factor();
+            times(own + 16 * (D::AS + 1));
 #pragma unroll
             for (int i = 0; i < 16; i++) put(16 * half + i, 16 * half + j, t[i]);
 #pragma unroll
-            for (int e = 0; e < 8; e++) put(16 + e / 4 * 8 + lane % 4 * 2 + e % 2, lane / 4 + e / 2 % 2 * 8, -m2[e / 4][e % 4]);
+            for (int e = 0; e < 8; e++) put(16 + e / 4 * 8 + lane % 4 * 2 + e % 2, lane / 4 + e / 2 % 2 * 8, -sum[e / 4][e % 4]);
             __syncwarp();
             bar_arrive(kInv + slot, STATE + 32);
         }
@@ -473,6 +477,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
         float u[NC][4] = {};
         {
             uint32_t xp[3][NC / 2][4];
+            float down[2];
 #pragma unroll
             for (int n = 0; n < NC; n++) {
                 const float4 w = *reinterpret_cast<const float4 *>(f + kXy * C + 2 * (n * 8 + lane % 4 * 2));   // B, .. of two rows
@@ -482,20 +487,24 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                     sk[n][e] = fmaf(e % 2 ? -w.w : -w.y, sk[n][e], (e % 2 ? w.z : w.x) * v);
                 }
             }
-            as_bf16<3>(sk, xp);
+            as_half(sk, xp, down);
             bar_sync(kInv + slot, STATE + 32);
 #pragma unroll
-            for (int m = 0; m < 3; m++) {   // rows n * 8 .. of T reach columns 0 .. n * 8 + 7
+            for (int m = 1; m >= 0; m--) {   // rows n * 8 .. of T reach columns 0 .. n * 8 + 7
                 uint32_t b[NC][4];
 #pragma unroll
                 for (int n = 0; n < NC; n++) ldsm4(b[n], at + D::TP + m * C * D::TS + (n * 8 + lane % 8) * D::TS + lane / 8 * 16);
 #pragma unroll
-                for (int l = 0; l < 3 - m; l++)
+                for (int l = 1 - m; l >= 0; l--)
 #pragma unroll
                     for (int kk = 0; kk < NC / 2; kk++)
 #pragma unroll
-                        for (int n = 2 * kk; n < NC; n++) mma16<B>(u[n], xp[l][kk], b[n][2 * kk], b[n][2 * kk + 1]);
+                        for (int n = 2 * kk; n < NC; n++) mma16<__half>(u[n], xp[l][kk], b[n][2 * kk], b[n][2 * kk + 1]);
             }
+#pragma unroll
+            for (int n = 0; n < NC; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) u[n][e] *= down[e / 2];
         }
         // the states after the chunk
         const float total = f[kTotal * C];
