@@ -42,17 +42,19 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
 }
 
 // A block: 128 outputs of NT tokens.  Rows of the product are outputs, so that a warp's stores of a token are side by
-// side.  Inputs go in stages of 256, 128 bytes a row.
+// side.  Inputs go in stages of 256, 128 bytes a row.  Two blocks share an SM, so that one's end (its sums' way out, about
+// a quarter of its products' time at 8192 inputs) lies under the other's products: one block of 256 tokens, whose products
+// need less of shared memory's bandwidth, took 161 us for 4096 x 8192 x 8192 where these take 147.
 template <int NT> struct Mx4Shape {
-    static constexpr int ST = NT == 128 ? 3 : NT <= 32 ? 5 : 4;   // stages; two blocks an SM up to 128 tokens
-    static constexpr int NB = (NT + 127) / 128;              // blocks of 128 tokens
+    static constexpr int ST = NT == 128 ? 3 : 4;             // stages
     static constexpr int A = 128 * 128, B = NT * 128;        // bytes of a stage
-    static constexpr int SF = 1024 * (1 + NB);               // of its scales: two words of four for each row
-    static constexpr int SMEM = ST * (A + B + SF) + 1024 /* alignment */ + 256 /* barriers */;
+    static constexpr int SF = 1024;                          // of each factor's scales: two words of four for each row
+    static constexpr int SMEM = ST * (A + B + 2 * SF) + 1024 /* alignment */ + 256 /* barriers */;
     static constexpr int ACC = NT < 32 ? 32 : NT;
-    static constexpr int SFC = 8 * (1 + NB);                 // columns of a stage's scales
-    static constexpr int COLS = ACC + ST * SFC <= 128 ? 128 : ACC + ST * SFC <= 256 ? 256 : 512;
+    static constexpr int SFC = 16;                           // columns of a stage's scales
+    static constexpr int COLS = ACC + ST * SFC <= 128 ? 128 : 256;
     static_assert(ST * (A + B) >= 128 * NT * 4, "the sums of a split product take the stages' place");
+    static_assert(2 * (SMEM + 1024) <= 228 * 1024 && ACC + ST * SFC <= COLS, "two blocks an SM");
 };
 
 // The 16 scale codes of `rows` rows for one chunk of 512 inputs, by a warp: on their way to shared memory as 4 blocks
@@ -159,17 +161,17 @@ __device__ __forceinline__ void mx4_put(const Mx4MatmulArgs &a, int t, int o, in
         if (i < n) y[i * a.ld_y] = Storage<T>::from_f(v[i]);
 }
 
-// Warp 0 asks for the factors (TMA), warp 1 multiplies, warps 4 to 6 bring the scales to shared memory, from where warp
+// Warp 0 asks for the factors (TMA), warp 1 multiplies, warps 4 and 5 bring the scales to shared memory, from where warp
 // 1 has them copied to tensor memory ahead of its products, and warps 4 to 7 finish.  A bounded wait that runs out ends
 // the block with NaN for its outputs.
-template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const __grid_constant__ Mx4MatmulArgs a) {
+template <int NT> __global__ void __launch_bounds__(256, 2) mx4_matmul_kernel(const __grid_constant__ Mx4MatmulArgs a) {
     using S = Mx4Shape<NT>;
     extern __shared__ unsigned char raw[];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ unsigned error;
     const uint32_t base = (tc::smem_u32(raw) + 1023) & ~1023u;
-    const uint32_t at_a = base, at_b = at_a + S::ST * S::A, at_sf = at_b + S::ST * S::B, bars = at_sf + S::ST * S::SF;
+    const uint32_t at_a = base, at_b = at_a + S::ST * S::A, at_sf = at_b + S::ST * S::B, bars = at_sf + S::ST * 2 * S::SF;
     const uint32_t full = bars, sf_full = bars + 8 * S::ST, empty = bars + 16 * S::ST, done = bars + 24 * S::ST;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const unsigned tile = blockIdx.x / a.split, rank = blockIdx.x % a.split, tiles_m = (unsigned)(a.m + NT - 1) / NT;
@@ -181,7 +183,7 @@ template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const
         abort_flag = 0, error = 0;
         for (int i = 0; i < S::ST; i++) {
             tc::mbar_init(full + 8 * i, 1);
-            tc::mbar_init(sf_full + 8 * i, 1 + S::NB);
+            tc::mbar_init(sf_full + 8 * i, 2);
             tc::mbar_init(empty + 8 * i, 1);
         }
         tc::mbar_init(done, 1);
@@ -221,28 +223,27 @@ template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const
                 const uint32_t phase = (it / S::ST) & 1;
                 if (!wait(full + 8 * s, phase) || !wait(sf_full + 8 * s, phase)) break;
                 tc::tc_fence_after();
-                const uint32_t sf = at_sf + s * S::SF, sfa = sft + s * S::SFC, sfb = sfa + 8;
+                const uint32_t sf = at_sf + s * 2 * S::SF, sfa = sft + s * S::SFC, sfb = sfa + 8;
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
                     copy_scales(sfa + k * 4, sf + k * 512);
-#pragma unroll
-                    for (int h = 0; h < S::NB; h++) copy_scales(sfb + (k * S::NB + h) * 4, sf + 1024 * (1 + h) + k * 512);
+                    copy_scales(sfb + k * 4, sf + S::SF + k * 512);
                 }
                 const uint64_t ad = tc::sw128_kmajor_desc(at_a + s * S::A), bd = tc::sw128_kmajor_desc(at_b + s * S::B);
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     mma_mx4(tmem, tc::desc_advance(ad, j * 32), tc::desc_advance(bd, j * 32), idesc_mx4(NT, (j & 1) * 2),
-                            sfa + j / 2 * 4, sfb + j / 2 * 4 * S::NB, (it | j) != 0);
+                            sfa + j / 2 * 4, sfb + j / 2 * 4, (it | j) != 0);
                 tc::mma_commit(empty + 8 * s);
             }
             tc::mma_commit(done);
         }
     } else if (warp >= 4) {
-        const int role = warp - 4;   // 0: weights' scales, 1 ..: tokens'
-        if (role <= S::NB) {
+        const int role = warp - 4;   // 0: weights' scales, 1: tokens'
+        if (role < 2) {
             const uint8_t *src = role ? a.xs : a.ws;
-            const int vec = role ? a.xvec : a.wvec, row0 = role ? m0 + (role - 1) * 128 : o0;
-            const int last = (role ? a.m : a.out) - 1, rows = role ? min(NT, 128) : 128;
+            const int vec = role ? a.xvec : a.wvec, row0 = role ? m0 : o0;
+            const int last = (role ? a.m : a.out) - 1, rows = role ? NT : 128;
             ScaleChunk chunk[2];
             bool ok = true;
             auto stage_pair = [&](const ScaleChunk &now, int it) {
@@ -253,7 +254,7 @@ template <int NT> __global__ void __launch_bounds__(256) mx4_matmul_kernel(const
                     if (it + h >= S::ST) ok = wait(empty + 8 * s, ((it + h) / S::ST - 1) & 1);
                     ok = __all_sync(~0u, ok);
                     if (!ok) break;
-                    now.store(at_sf + s * S::SF + role * 1024, vec, h, lane);
+                    now.store(at_sf + (2 * s + role) * S::SF, vec, h, lane);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(sf_full + 8 * s);
@@ -365,9 +366,13 @@ static cudaError_t run_mx4(Mx4MatmulArgs &a, const void *wq, const void *xq, int
         attr.store(ctx, std::memory_order_relaxed);
     }
     const long long tiles = (long long)((a.m + NT - 1) / NT) * ((a.out + 127) / 128);
-    const int fit = S::COLS == 512 || S::SMEM > 113 * 1024 ? 1 : 2;
+    // Blocks that share the inputs of a tile, where the tiles leave SMs without a block.  More than four, and for 128
+    // tokens a second block an SM, cost more than they bring.  Measured, us without sharing, with two, four and eight: 16
+    // tokens, 4096 x 4096 (32 tiles) 9.2, -, 6.5, 8.4; 300 tokens, 1000 x 8192 (24) 19.7, -, 11.8, 12.7; 16 tokens, 8192 x
+    // 8192 (64) 16.2, 11.5, 10.8; 256 tokens, 8192 x 4096 (128) 12.1, 14.2; 333 tokens, 5003 x 4128 (120) 15.8, 18.0.
+    const long long most = (long long)sms * (NT < 128 ? 2 : 1);
     a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= (long long)sms * fit && 2 * a.split <= a.chunks) a.split *= 2;
+    while (a.split < 4 && tiles * a.split * 2 <= most && 2 * a.split <= a.chunks) a.split *= 2;
     return launch(mx4_matmul_kernel<NT>, dim3((unsigned)(tiles * a.split)), 256, S::SMEM, st, a, a.split);
 }
 
@@ -410,12 +415,10 @@ extern "C" fcm_status fcm_mx4_matmul(const fcm_mx4_matmul_desc *desc, const void
     a.chunks = (int)((groups + 15) / 16);
     a.wvec = seq::aligned16(ws) && groups % 16 == 0, a.xvec = seq::aligned16(xs) && groups % 16 == 0;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const long long tiles256 = (((long long)d.m + 255) / 256) * ((d.out + 127) / 128);
-    const cudaError_t ce = d.m <= 16    ? seq::run_mx4<16>(a, wq, xq, sms, cs)
-                           : d.m <= 32  ? seq::run_mx4<32>(a, wq, xq, sms, cs)
-                           : d.m <= 64  ? seq::run_mx4<64>(a, wq, xq, sms, cs)
-                           : d.m <= 128 || tiles256 < sms ? seq::run_mx4<128>(a, wq, xq, sms, cs)
-                                                          : seq::run_mx4<256>(a, wq, xq, sms, cs);
+    const cudaError_t ce = d.m <= 16   ? seq::run_mx4<16>(a, wq, xq, sms, cs)
+                           : d.m <= 32 ? seq::run_mx4<32>(a, wq, xq, sms, cs)
+                           : d.m <= 64 ? seq::run_mx4<64>(a, wq, xq, sms, cs)
+                                       : seq::run_mx4<128>(a, wq, xq, sms, cs);
     if (ce != cudaSuccess) return fcm_fail(FCM_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(ce));
     return FCM_OK;
 }
