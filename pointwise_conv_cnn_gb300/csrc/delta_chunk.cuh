@@ -129,7 +129,7 @@ template <typename T> __device__ __forceinline__ uint4 load_keys(const T *p, int
     return v;
 }
 
-// 16 bytes from global to shared memory without a register; zeros where there is no row.
+// 16 bytes from global to shared memory without a register; zeros where there is no row: then nothing is read.
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
 }
@@ -184,12 +184,13 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             unsigned char *plain = smem + (to - base);
             const int left = len - c * C - r0;   // rows of this thread's, RPP apart
             const T *k = k_at, *q = q_at;
+            const bool in = col < a.dk;
 #pragma unroll
             for (int p = 0; p < PASS; p++) {
                 const bool live = p * RPP < left;
                 if (a.vec) {
-                    copy16(to + p * RPP * D::KS, live ? k : kp, live && col < a.dk);
-                    copy16(to + D::Q + p * RPP * D::KS, live ? q : qp, live && col < a.dk);
+                    copy16(to + p * RPP * D::KS, k, live && in);
+                    copy16(to + D::Q + p * RPP * D::KS, q, live && in);
                 } else {
                     *reinterpret_cast<uint4 *>(plain + p * RPP * D::KS) = load_keys(k - (col < a.dk ? col : 0), col, a.dk, live, false);
                     *reinterpret_cast<uint4 *>(plain + D::Q + p * RPP * D::KS) = load_keys(q - (col < a.dk ? col : 0), col, a.dk, live, false);
@@ -198,7 +199,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             }
             k_at = k, q_at = q;   // PASS * RPP rows are a chunk
             const bool live = c * C + tid / 4 < len;
-            if (a.vec_v) copy16(to_v, live ? v_at : vp, live && vc < vcols);
+            if (a.vec_v) copy16(to_v, v_at, live && vc < vcols);
             else *reinterpret_cast<uint4 *>(smem + (to_v - base)) = load_keys(v_at - (vc < vcols ? vc : 0), vc, vcols, live, false);
             v_at += C * a.ld_v;
         };
