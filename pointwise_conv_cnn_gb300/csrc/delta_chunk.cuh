@@ -116,17 +116,12 @@ __device__ __forceinline__ void as_half(const float (&c)[N][4], uint32_t (&part)
             split2(c[i][2 * r] * up[r], c[i][2 * r + 1] * up[r], part[0][i / 2][i % 2 * 2 + r], part[1][i / 2][i % 2 * 2 + r]);
 }
 
-// Eight neighbouring keys or queries of a row, zeros past the row's end.
-template <typename T> __device__ __forceinline__ uint4 load_keys(const T *p, int e, int dk, bool live, bool vec) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (!live || e >= dk) return v;
-    if (vec) return *reinterpret_cast<const uint4 *>(p + e);
-    unsigned short s[8];
+// Up to eight neighbouring elements of a row, zeros past its end.
+template <typename T> __device__ __forceinline__ uint4 load_keys(const T *p, int n, bool live) {
+    uint32_t s[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) s[i] = e + i < dk ? reinterpret_cast<const unsigned short *>(p)[e + i] : (unsigned short)0;
-    v.x = s[0] | (uint32_t)s[1] << 16, v.y = s[2] | (uint32_t)s[3] << 16;
-    v.z = s[4] | (uint32_t)s[5] << 16, v.w = s[6] | (uint32_t)s[7] << 16;
-    return v;
+    for (int i = 0; i < 8; i++) s[i] = live && i < n ? reinterpret_cast<const unsigned short *>(p)[i] : 0u;
+    return make_uint4(s[0] | s[1] << 16, s[2] | s[3] << 16, s[4] | s[5] << 16, s[6] | s[7] << 16);
 }
 
 // 16 bytes from global to shared memory without a register; zeros where there is no row: then nothing is read.
@@ -183,24 +178,33 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             const uint32_t to = base + slot * D::SLOT + r0 * D::KS + col * 2, to_v = base + slot * D::SLOT + D::V + tid / 4 * D::TS + vc * 2;
             unsigned char *plain = smem + (to - base);
             const int left = len - c * C - r0;   // rows of this thread's, RPP apart
+            const bool in = col < a.dk, v_live = c * C + tid / 4 < len && vc < vcols;
             const T *k = k_at, *q = q_at;
-            const bool in = col < a.dk;
+            if (a.vec) {
 #pragma unroll
-            for (int p = 0; p < PASS; p++) {
-                const bool live = p * RPP < left;
-                if (a.vec) {
+                for (int p = 0; p < PASS; p++) {
+                    const bool live = p * RPP < left;
                     copy16(to + p * RPP * D::KS, k, live && in);
                     copy16(to + D::Q + p * RPP * D::KS, q, live && in);
-                } else {
-                    *reinterpret_cast<uint4 *>(plain + p * RPP * D::KS) = load_keys(k - (col < a.dk ? col : 0), col, a.dk, live, false);
-                    *reinterpret_cast<uint4 *>(plain + D::Q + p * RPP * D::KS) = load_keys(q - (col < a.dk ? col : 0), col, a.dk, live, false);
+                    k += k_row, q += q_row;
                 }
-                k += k_row, q += q_row;
+            } else {   // element by element, all on their way before the first is stored
+                uint4 ke[PASS], qe[PASS];
+#pragma unroll
+                for (int p = 0; p < PASS; p++) {
+                    const bool live = p * RPP < left && in;
+                    ke[p] = load_keys(k, a.dk - col, live), qe[p] = load_keys(q, a.dk - col, live);
+                    k += k_row, q += q_row;
+                }
+#pragma unroll
+                for (int p = 0; p < PASS; p++) {
+                    *reinterpret_cast<uint4 *>(plain + p * RPP * D::KS) = ke[p];
+                    *reinterpret_cast<uint4 *>(plain + D::Q + p * RPP * D::KS) = qe[p];
+                }
             }
             k_at = k, q_at = q;   // PASS * RPP rows are a chunk
-            const bool live = c * C + tid / 4 < len;
-            if (a.vec_v) copy16(to_v, v_at, live && vc < vcols);
-            else *reinterpret_cast<uint4 *>(smem + (to_v - base)) = load_keys(v_at - (vc < vcols ? vc : 0), vc, vcols, live, false);
+            if (a.vec_v) copy16(to_v, v_at, v_live);
+            else *reinterpret_cast<uint4 *>(smem + (to_v - base)) = load_keys(v_at, vcols - vc, v_live);
             v_at += C * a.ld_v;
         };
 #pragma unroll 1

@@ -51,16 +51,17 @@ template <int V> __device__ __forceinline__ void finish_channels(float (&v)[V], 
         for (int i = 0; i < V; i++) v[i] *= silu(z[i]);
     }
 }
-// V of s or b from channel d on, a multiple of V (16-byte aligned where V > 1), or the value that stands for none.
+// V of s or b from channel d on, a multiple of V (16-byte aligned where V >= 4), or the value that stands for none.
 template <int V> __device__ __forceinline__ void load_affine(const float *p, int d, float none, float (&v)[V]) {
-    if constexpr (V > 1) {
+    if constexpr (V >= 4) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
             const float4 x = p ? *reinterpret_cast<const float4 *>(p + d + i) : make_float4(none, none, none, none);
             v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
         }
     } else {
-        v[0] = p ? p[d] : none;
+#pragma unroll
+        for (int i = 0; i < V; i++) v[i] = p ? p[d + i] : none;
     }
 }
 // Channels d .. d + V - 1's mean and factor, by their groups'.
@@ -183,8 +184,11 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ void norm_copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+template <int BYTES> __device__ __forceinline__ void norm_copy(void *to, const void *from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
 }
 
 // Sums of V channels about a first value each, of which a large mean costs the squares nothing.
@@ -256,6 +260,11 @@ __device__ __forceinline__ void apply_rows(int n, int hold, const T *x, long lon
     }
 }
 
+// Where a shared sample's sums wait in its outputs: the first 16-byte boundary.
+__device__ __forceinline__ float *sums_of(void *y) {
+    return reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(y) + 15) & ~(uintptr_t)15);
+}
+
 // N lanes' counts, means and squares about the mean as those of all their values, in every lane; a count of 0 says nothing.
 template <int N> __device__ __forceinline__ void join_sums(float &n, float &m, float &q) {
     float total = n, sum = n > 0.0f ? n * m : 0.0f;
@@ -278,7 +287,8 @@ template <int N> __device__ __forceinline__ void join_sums(float &n, float &m, f
 constexpr int kMapThreads = 256;
 template <typename T, int V, bool GATE> __global__ void __launch_bounds__(kMapThreads, 2) norm_maps_kernel(const NormArgs a) {
     constexpr int U = 4, RING = 8, nt = kMapThreads, warps = nt / 32;
-    constexpr bool ASYNC = V * sizeof(T) == 16;
+    constexpr int BYTES = V * sizeof(T);
+    constexpr bool ASYNC = BYTES >= 4;   // single 16-bit channels go through registers
     extern __shared__ __align__(16) unsigned char smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     float *part_m = reinterpret_cast<float *>(smem), *part_q = part_m + nt * V;   // [TY][a pass's channels, joined]
@@ -311,27 +321,31 @@ template <typename T, int V, bool GATE> __global__ void __launch_bounds__(kMapTh
                 const int at = i < passing ? (i - passing) & (RING - 1) : i - passing;   // RING divides 2^32
                 return kept + ((size_t)(ty + at * ty_n) * cols + col) * V;
             };
-            if (ASYNC && a.async) {
-                const uint32_t to = tc::smem_u32(kept + ((size_t)ty * cols + col) * V), round = ty_n * cols * 16;
-                auto at = [&](int i) { return to + (uint32_t)(i < passing ? (i - passing) & (RING - 1) : i - passing) * round; };
-                const T *kept_from = x + (long long)ty * a.ld_x + col * V, *from = kept_from + (long long)hold * ty_n * a.ld_x;
-                const long long step = ty_n * a.ld_x;
-                if (passing == 0) from = kept_from;
+            bool done = false;
+            if constexpr (ASYNC)
+                if (a.async) {
+                    T *const to = kept + ((size_t)ty * cols + col) * V;
+                    const int round = ty_n * cols * V;
+                    auto at = [&](int i) { return to + (i < passing ? (i - passing) & (RING - 1) : i - passing) * round; };
+                    const T *kept_from = x + (long long)ty * a.ld_x + col * V, *from = kept_from + (long long)hold * ty_n * a.ld_x;
+                    const long long step = ty_n * a.ld_x;
+                    if (passing == 0) from = kept_from;
 #pragma unroll 1
-                for (int i = -RING; i < mine; i++) {
-                    if (i >= 0) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
-                        const uint4 raw = tc::lds128(at(i));
-                        float v[V];
-                        reinterpret_cast<const Vec<T, V> &>(raw).get(v);
-                        if (i == 0 && !a.rms) s.start(v);
-                        s.add(v);
+                    for (int i = -RING; i < mine; i++) {
+                        if (i >= 0) {
+                            asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+                            float v[V];
+                            reinterpret_cast<const Vec<T, V> *>(at(i))->get(v);
+                            if (i == 0 && !a.rms) s.start(v);
+                            s.add(v);
+                        }
+                        if (i + RING < mine) norm_copy<BYTES>(at(i + RING), from);
+                        from = i + RING + 1 == passing ? kept_from : from + step;
+                        asm volatile("cp.async.commit_group;" ::: "memory");
                     }
-                    if (i + RING < mine) norm_copy16(at(i + RING), from);
-                    from = i + RING + 1 == passing ? kept_from : from + step;
-                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    done = true;
                 }
-            } else {
+            if (!done) {
 #pragma unroll 1
                 for (int i = 0; i < mine; i += U) {
                     Vec<T, V> raw[U];
@@ -405,7 +419,7 @@ template <typename T, int V, bool GATE> __global__ void __launch_bounds__(kMapTh
             if (!a.parts) {
                 mean_of[g] = a.rms ? 0.0f : m, factor_of[g] = rsqrtf(__fdividef(q, n) + a.eps);
             } else if (rank == 0) {
-                float *begin = reinterpret_cast<float *>(static_cast<T *>(a.y) + (long long)sample * a.pixels * a.c);
+                float *begin = sums_of(static_cast<T *>(a.y) + (long long)sample * a.pixels * a.c);
                 float *to = begin + 4 + 3 * ((long long)part * a.groups + g);
                 to[0] = n, to[1] = m, to[2] = q;
                 if (part == 0 && g == 0) *reinterpret_cast<unsigned *>(begin) = 0;
@@ -449,7 +463,7 @@ template <typename T, int V, bool GATE> __global__ void __launch_bounds__(256, 2
     const long long begin = (long long)sample * a.pixels;
     tc::pdl_wait();
     tc::pdl_launch_dependents();
-    float *sums = reinterpret_cast<float *>(static_cast<T *>(a.y) + begin * a.c) + 4;
+    float *sums = sums_of(static_cast<T *>(a.y) + begin * a.c) + 4;
     // a warp's next group is on its way while one is joined
     auto load = [&](int g, float (&v)[3]) {
         const float *p = sums + 3 * ((long long)min(lane, a.parts - 1) * a.groups + min(g, a.groups - 1));
@@ -529,14 +543,14 @@ template <typename T, int V> static cudaError_t run_shared(NormArgs a, int sms, 
     a.ppc = (a.pixels + a.parts * CL - 1) / (a.parts * CL);
     cudaError_t e = launch_maps<T, V>(a, (long long)a.n * a.parts * CL, fixed + (a.async ? ring : 0), CL, st);
     if (e != cudaSuccess) return e;
-    a.skip = (16 + 12ll * a.parts * a.groups + row - 1) / row;
+    a.skip = (32 + 12ll * a.parts * a.groups + row - 1) / row;
     const long long blocks = 4ll * sms / a.n + 1, rest = a.pixels - a.skip;
     a.ppc = (rest + blocks - 1) / blocks;
     a.nb = (int)((rest + a.ppc - 1) / a.ppc);
     return launch(a.z ? norm_apply_kernel<T, V, true> : norm_apply_kernel<T, V, false>, dim3((unsigned)(a.n * a.nb)), 256, stats, st, a);
 }
 
-template <typename T, int V> static cudaError_t run_maps(NormArgs a, int sms, cudaStream_t st) {
+template <typename T, int V> static cudaError_t run_maps(NormArgs a, bool may_share, int sms, cudaStream_t st) {
     // Whole vectors of whole groups.
     long long unit = a.cpg;
     while (unit % V) unit += a.cpg;
@@ -553,6 +567,14 @@ template <typename T, int V> static cudaError_t run_maps(NormArgs a, int sms, cu
         else if (few && nb < units && seg(2 * nb) >= 32) nb *= 2;
         else break;
     }
+    // Whether clusters share samples instead, which costs two launches and the joining of their sums, some 30 us.  A block
+    // takes 1.1 ns a vector and so does an SM (measured from 40000 x 66 in pairs of channels, 204 us by 8 blocks, to 512 x
+    // 512 x 128, 62 shared).  What the blocks' shared memory does not keep is read again, at half the speed: a sample of
+    // 40000 x 128 21 us and 33 shared, 90000 x 128 53 and 39; 32 samples of 8192 x 128 106 and 75, 16 32 and 51.
+    const double sample = (double)a.pixels * a.c, vectors = sample / V, blocks = (double)nb * cl, bytes = sample * sizeof(T);
+    if (may_share && (1.1e-3 * vectors / blocks > 35.0 + 1.1e-3 * vectors * a.n / sms || bytes > 16e6 ||
+                      (bytes > 1.5e6 && bytes * a.n > 38e6)))
+        return run_shared<T, V>(a, sms, st);
     const int per = (units + nb - 1) / nb;
     a.cb = (int)(per * unit), a.nb = (units + per - 1) / per;
     a.ppc = (a.pixels + cl - 1) / cl;
@@ -571,13 +593,6 @@ template <typename T, int V, int LPG, int NV, int ROWS> static cudaError_t rows_
     return launch(norm_rows_kernel<T, V, LPG, NV, ROWS>, dim3((unsigned)((units * LPG + 255) / 256)), 256, 0, st, a);
 }
 
-// Whether clusters share samples.  One cluster keeps up to 1.5 MB; beyond that, the blocks' shared memory (30 MB) and L2
-// carry a batch a while further.
-static bool shared_sample(const NormArgs &a, size_t e) {
-    const double bytes = (double)a.pixels * a.c * e;
-    return bytes > 1.5e6 && (bytes > 16e6 || bytes * a.n > 38e6) && a.groups <= 2048;
-}
-
 template <typename T> static cudaError_t run_norm(const NormArgs &a, int sms, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     const bool vec = aligned16(a.x) && aligned16(a.y) && aligned16(a.z) && aligned16(a.s) && aligned16(a.b) &&
@@ -592,8 +607,15 @@ template <typename T> static cudaError_t run_norm(const NormArgs &a, int sms, cu
     }
     if (a.pixels == 1 && a.cpg <= 256)
         return a.cpg <= 64 ? rows_kernel<T, 1, 32, 2, 4>(a, st) : rows_kernel<T, 1, 32, 8, 2>(a, st);
-    if (vec && a.x != a.y && a.ld_y == a.c && shared_sample(a, sizeof(T))) return run_shared<T, V>(a, sms, st);
-    return vec ? run_maps<T, V>(a, sms, st) : run_maps<T, 1>(a, sms, st);
+    // a shared sample's sums need room in outputs that are not inputs, and few pixels of it
+    const bool may_share = a.x != a.y && a.ld_y == a.c && a.groups <= 2048 && a.pixels >= 4096;
+    if (vec) return run_maps<T, V>(a, may_share, sms, st);
+    if constexpr (sizeof(T) == 2) {   // two channels at once
+        const auto at4 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; };
+        if (at4(a.x) && at4(a.y) && at4(a.z) && ((a.ld_x | a.ld_y | (a.z ? a.ld_z : 0) | a.c) % 2) == 0)
+            return run_maps<T, 2>(a, may_share, sms, st);
+    }
+    return run_maps<T, 1>(a, may_share, sms, st);
 }
 
 }  // namespace seq

@@ -152,7 +152,7 @@ def test_calls_on_two_streams_at_once():
 
 @pytest.mark.parametrize("n,pixels,c,dtype,kernel,count", [
     (1, 90000, 128, torch.bfloat16, "norm_apply", 2), (1, 3000, 128, torch.bfloat16, "norm_maps", 1),
-    (4000, 1, 256, torch.bfloat16, "norm_rows", 1), (1, 90000, 127, torch.bfloat16, "norm_maps", 1)])
+    (4000, 1, 256, torch.bfloat16, "norm_rows", 1), (1, 90000, 127, torch.bfloat16, "norm_apply", 2)])
 def test_norm_kernels_by_size(n, pixels, c, dtype, kernel, count):
     x = torch.zeros((n, pixels, c), dtype=dtype, device="cuda")
     y = torch.empty_like(x)
