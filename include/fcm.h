@@ -445,9 +445,10 @@ FCM_API fcm_status fcm_w4_matvec(const fcm_w4_desc *desc, const void *x, const v
  * [heads] float32 (dt_bias may be NULL: 0).  state_in / state_out [slots][heads][dk][dv] float32 hold S before and
  * after; state_in NULL starts from zeros, state_out NULL keeps nothing.  dk 1 to 256, dv from 1 on; key_heads divides
  * heads.  Any dt and a are taken, infinite ones too: e^G is 0 below G = -104, and the state grows where G > 0.
- * Prompts go through in chunks of rows, whose products meet each other before any sum: a NaN or an infinity among a
- * head's rows, states or decays may therefore make any row of that head and sequence NaN, earlier ones of the same
- * chunk too, as may factors e^G whose product over 64 rows leaves a float's range. */
+ * Prompts (16-bit types, dk up to 128, a longest sequence of 16 rows or more) go through in chunks of 32 rows, whose
+ * products meet each other before any sum: a NaN or an infinity among a head's rows, states or decays may therefore make
+ * any row of that head and sequence from the chunk's first on NaN, as may factors whose product over a chunk's rows leaves a float's
+ * range, or keys that are not normalised where the rule multiplies what it was told by more than 65504 within 32 rows. */
 typedef struct fcm_delta_desc {
     fcm_seqs seqs;
     int heads, key_heads, dk, dv, dtype, softplus, sigmoid, normalize;

@@ -77,7 +77,8 @@ template <int V, typename F> __device__ __forceinline__ void by_group(int d, int
 // ---------------------------------------------------------------------------------- rows
 // One pixel: LPG lanes hold a row's group, NV times V channels each, and sum it twice in registers: its
 // mean, then the squares about it.  A thread has the same group of ROWS rows, all on their way at once, with
-// s and b read once.
+// s and b read once.  Bound by memory: 8192 rows of 32 heads of 128 with a gate, 201 MB in 42.5 us, 4.7 TB/s, 0.70 of a
+// plain copy's rate.
 template <typename T, int V, int LPG, int NV, int ROWS>
 __global__ void __launch_bounds__(256) norm_rows_kernel(const NormArgs a) {
     tc::pdl_wait();
@@ -453,7 +454,8 @@ template <typename T, int V, bool GATE> __global__ void __launch_bounds__(kMapTh
 }
 
 // The second step of samples that clusters share (run_shared): their sums joined, the pixels normalised.  The block that
-// is the last to have read a sample's sums also writes the pixels that they lie in.
+// is the last to have read a sample's sums also writes the pixels that they lie in.  512 x 512 x 128 bf16: 25 us for the
+// sums (2.6 TB/s) and 37 for this (3.6 TB/s): x comes from memory twice, since the L2's halves do not hold its 67 MB.
 template <typename T, int V, bool GATE> __global__ void __launch_bounds__(256, 2) norm_apply_kernel(const NormArgs a) {
     extern __shared__ float stats[];   // mean and factor of each group
     __shared__ bool last;
