@@ -355,7 +355,8 @@ FCM_API fcm_status fcm_fuse_plan(const fcm_layer *layers, int n_layers, int batc
  *    `stream` and return.  What the host cannot see (seq_start, slot) is bounded by the kernels
  *    as said below: no value in them makes a kernel read or write outside the tensors described
  *    (but for the bytes before a row in the aligned 16-byte piece that it starts in, 14 at most,
- *    which the scan loads and does not use).
+ *    which the scan loads and does not use, and those beside a row of scale codes in the aligned words
+ *    that it lies in, 3 at most on either side, as fcm_mx4_matmul does).
  *  - Activations are rows of channels, one row per token, `ld_*` elements apart (0: the row's
  *    own length, rows contiguous), so a layer reads and writes column blocks of wider tensors.
  *    16-byte aligned pointers and row distances run fastest; any others are served.
@@ -465,7 +466,8 @@ FCM_API fcm_status fcm_gated_delta(const fcm_delta_desc *desc, const void *q, co
  * mean and var over a sample's pixels and a group's channels; rms 1: mean is 0 and var the mean of squares.  x, z, y
  * [n][pixels][c], all n * pixels rows ld_* apart; s, b [c] float32; s, b, z may be NULL (1, 0, no gate).  y may be x
  * itself (the same pointer and row distance).  pixels 1 normalises a row's groups each by itself: the heads of a
- * layer over sequences.  eps >= 0; NaN and infinities stay in their sample and group. */
+ * layer over sequences.  eps >= 0, c at most 8192; NaN and infinities stay in their sample and
+ * group.  While a call runs, y's first pixels of a large sample may hold its sums. */
 typedef struct fcm_norm_desc {
     int n, c, groups, dtype, act, rms;
     float eps;
@@ -477,7 +479,8 @@ FCM_API fcm_status fcm_group_norm(const fcm_norm_desc *desc, const void *x, cons
 /* Microscaled 4-bit floating point (OCP microscaling format, E2M1 values): rows of `in` values in blocks of 32 that
  * share a power of two.  q [rows][in/2] bytes, the value of an even place in the low four bits of byte i/2 and the
  * next one's in the high four: codes 0 to 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, with 8 added for their negatives.
- * s [rows][in/32] bytes: code e stands for 2^(e-127), 255 for NaN.  in is a multiple of 32.  q and s are contiguous.
+ * s [rows][in/32] bytes: code e stands for 2^(e-127), 255 for NaN.  in is a multiple of 32.  q and s are contiguous, q
+ * 4-byte aligned.
  *
  * Quantising takes x [m][in] (ld_x apart; FCM_F32, FCM_F16, FCM_BF16): a block's power is 2^(floor(log2(largest
  * magnitude)) - 2), at least 2^-127, and each value the nearest one after division by it, ties to the even code,
@@ -494,7 +497,8 @@ FCM_API fcm_status fcm_mx4_dequantize(const fcm_mx4_desc *desc, const void *q, c
  *     y[t,o] = act(s[o] * sum_i x[t,i] * w[o,i] + b[o])
  * xq, xs: the m rows; wq, ws: the `out` rows of weights (both as fcm_mx4_quantize leaves them; xq and wq 16-byte
  * aligned); y [m][out] in FCM_F32, FCM_F16 or FCM_BF16; s, b [out] float32 (NULL: 1, 0).  Sums are float32.  A block
- * of code 255 makes NaN of its row's sums. */
+ * of code 255 makes NaN of its row's sums.  The kernel's waits for its own copies and products are bounded: one that
+ * runs out (after a second; none is expected to) leaves NaN in the outputs it concerns. */
 typedef struct fcm_mx4_matmul_desc {
     int m, out, in, dtype, act;
     long long ld_y;

@@ -55,8 +55,8 @@ __global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const D
     const T *vp = static_cast<const T *>(a.vp) + (size_t)h * a.dv + d0;
     T *y = static_cast<T *>(a.y) + (size_t)h * a.dv + d;
     const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-    for (int b0 = 0; b0 < len; b0 += TB) {
-        const int n = min(TB, len - b0);
+    for (int b0 = 0, n; b0 < len; b0 += n) {
+        n = min(TB, len - b0);
         const long long t = t0 + b0;
         for (int i = threadIdx.x; i < n * DK; i += 128) {
             const int j = i / DK, e = i % DK;

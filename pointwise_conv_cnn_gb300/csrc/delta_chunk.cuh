@@ -171,7 +171,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
     long long t0;
     int len;
     seq_rows(a.q, q, t0, len);
-    const int chunks = (len + C - 1) / C;
+    const int chunks = len / C + (len % C != 0);
     auto factors = [&](int slot) { return reinterpret_cast<float *>(smem + slot * D::SLOT + D::SC); };
 
     if (warp >= D::STATE && warp < D::STATE + D::FRONT) {
