@@ -96,11 +96,18 @@ template <int M, int N> __device__ __forceinline__ void as_bf16(const float (&c)
 // `down` undoes it.
 template <int N>
 __device__ __forceinline__ void as_half(const float (&c)[N][4], uint32_t (&part)[3][N / 2][4], float (&down)[2]) {
-    uint32_t top[2] = {};
+    uint32_t top[2];
 #pragma unroll
-    for (int i = 0; i < N; i++)
+    for (int r = 0; r < 2; r++) {
+        uint32_t m[N];
 #pragma unroll
-        for (int e = 0; e < 4; e++) top[e / 2] = max(top[e / 2], magnitude(c[i][e]));
+        for (int i = 0; i < N; i++) m[i] = max(magnitude(c[i][2 * r]), magnitude(c[i][2 * r + 1]));
+#pragma unroll
+        for (int s = N / 2; s; s /= 2)
+#pragma unroll
+            for (int i = 0; i < s; i++) m[i] = max(m[i], m[i + s]);
+        top[r] = m[0];
+    }
     float up[2];
 #pragma unroll
     for (int r = 0; r < 2; r++) {
@@ -276,6 +283,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             }
 #pragma unroll
             for (int n = 0; n < 4; n++) {
+                if (n == 2 && m0 == 0) break;   // no row before the 16th reaches these, and none is read
                 const float2 hj = *reinterpret_cast<const float2 *>(f + kSumHi * C + n * 8 + j0);
                 const float2 lj = *reinterpret_cast<const float2 *>(f + kSumLo * C + n * 8 + j0);
                 const float2 kj = *reinterpret_cast<const float2 *>(f + kToEnd * C + n * 8 + j0);
@@ -426,7 +434,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             S[n][e] = a.state_in && row >= 0 && k < a.dk && d0 + d < a.dv ? a.state_in[cell + (size_t)k * a.dv + d] : 0.0f;
         }
     const uint32_t meet = base + D::SLOTS * D::SLOT + pair * DS * 8 * 512 + lane * 16;
-    T *y = static_cast<T *>(a.y) + (size_t)h * a.dv + d0 + rd;
+    T *y_at = static_cast<T *>(a.y) + (size_t)h * a.dv + d0 + rd + (t0 + part * 8 + lane % 4 * 2) * a.ld_y;   // a lane's first row
     const bool in0 = d0 + rd < a.dv, in1 = d0 + rd + 8 < a.dv;
     for (int c = 0; c < chunks; c++) {
         const int slot = c % D::SLOTS;
@@ -580,7 +588,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 }
                 const int r = n * 8 + lane % 4 * 2, live = len - c * C - r;   // rows r and r + 1
                 const float2 reach = *reinterpret_cast<const float2 *>(f + kQReach * C + r);
-                T *to = y + (t0 + c * C + r) * a.ld_y;
+                T *to = y_at + i * 16 * a.ld_y;
                 if (live > 0 && in0) to[0] = Storage<T>::from_f(fmaf(yq[i][0], reach.x, w[0]));
                 if (live > 0 && in1) to[8] = Storage<T>::from_f(fmaf(yq[i][2], reach.x, w[2]));
                 to += a.ld_y;
@@ -588,6 +596,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 if (live > 1 && in1) to[8] = Storage<T>::from_f(fmaf(yq[i][3], reach.y, w[3]));
             }
         }
+        y_at += C * a.ld_y;
         if (c + D::SLOTS < chunks) bar_arrive(kFree + slot, STATE + FRONT);
     }
     if (a.state_out && row >= 0) {

@@ -455,7 +455,7 @@ template <typename T, int V, bool GATE> __global__ void __launch_bounds__(kMapTh
 
 // The second step of samples that clusters share (run_shared): their sums joined, the pixels normalised.  The block that
 // is the last to have read a sample's sums also writes the pixels that they lie in.  512 x 512 x 128 bf16: 25 us for the
-// sums (2.6 TB/s) and 37 for this (3.6 TB/s): x comes from memory twice, since the L2's halves do not hold its 67 MB.
+// sums (2.6 TB/s) and 30 for this (4.5 TB/s of x and y); two rounds of blocks, which all join the sums first, took 38.
 template <typename T, int V, bool GATE> __global__ void __launch_bounds__(256, 2) norm_apply_kernel(const NormArgs a) {
     extern __shared__ float stats[];   // mean and factor of each group
     __shared__ bool last;
@@ -463,6 +463,7 @@ template <typename T, int V, bool GATE> __global__ void __launch_bounds__(256, 2
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int sample = blockIdx.x / a.nb, block = blockIdx.x % a.nb;   // nb: blocks of a sample
     const long long begin = (long long)sample * a.pixels;
+    const long long p0 = a.skip + block * a.ppc, p1 = min(p0 + a.ppc, a.pixels);
     tc::pdl_wait();
     tc::pdl_launch_dependents();
     float *sums = sums_of(static_cast<T *>(a.y) + begin * a.c) + 4;
@@ -501,7 +502,6 @@ template <typename T, int V, bool GATE> __global__ void __launch_bounds__(256, 2
             apply_rows<T, V, 4, GATE>(mine, 0, xp, ty_n * a.ld_x, xp, 0, zp, ty_n * a.ld_z, yp, (long long)ty_n * a.c, m, f, b, a.act);
         }
     };
-    const long long p0 = a.skip + block * a.ppc, p1 = min(p0 + a.ppc, a.pixels);
     __syncthreads();
     const int turns = last ? 2 : 1;
     __threadfence();
@@ -546,7 +546,8 @@ template <typename T, int V> static cudaError_t run_shared(NormArgs a, int sms, 
     cudaError_t e = launch_maps<T, V>(a, (long long)a.n * a.parts * CL, fixed + (a.async ? ring : 0), CL, st);
     if (e != cudaSuccess) return e;
     a.skip = (32 + 12ll * a.parts * a.groups + row - 1) / row;
-    const long long blocks = 4ll * sms / a.n + 1, rest = a.pixels - a.skip;
+    // as many blocks as are on the SMs at once: each joins the sums first
+    const long long blocks = a.n < 2 * sms ? 2ll * sms / a.n : 1, rest = a.pixels - a.skip;
     a.ppc = (rest + blocks - 1) / blocks;
     a.nb = (int)((rest + a.ppc - 1) / a.ppc);
     return launch(a.z ? norm_apply_kernel<T, V, true> : norm_apply_kernel<T, V, false>, dim3((unsigned)(a.n * a.nb)), 256, stats, st, a);
