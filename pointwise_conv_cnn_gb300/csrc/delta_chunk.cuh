@@ -123,6 +123,12 @@ __device__ __forceinline__ void as_half(const float (&c)[N][4], uint32_t (&part)
             split2(c[i][2 * r] * up[r], c[i][2 * r + 1] * up[r], part[0][i / 2][i % 2 * 2 + r], part[1][i / 2][i % 2 * 2 + r]);
 }
 
+// Two 16-bit elements in 32 bits each.
+template <typename T> __device__ __forceinline__ float2 two_of(uint32_t v) {
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    else return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
 // Up to eight neighbouring elements of a row, zeros past its end.
 template <typename T> __device__ __forceinline__ uint4 load_keys(const T *p, int n, bool live) {
     uint32_t s[8];
@@ -199,7 +205,14 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             const int left = len - c * C - r0;   // rows of this thread's, RPP apart
             const bool in = col < a.dk, v_live = c * C + tid / 4 < len && vc < vcols;
             const T *k = k_at, *q = q_at;
-            if (a.vec) {
+            if (a.vec && in && left >= C - r0) {   // a whole chunk's rows
+#pragma unroll
+                for (int p = 0; p < PASS; p++) {
+                    copy16(to + p * RPP * D::KS, k, true);
+                    copy16(to + D::Q + p * RPP * D::KS, q, true);
+                    k += k_row, q += q_row;
+                }
+            } else if (a.vec) {
 #pragma unroll
                 for (int p = 0; p < PASS; p++) {
                     const bool live = p * RPP < left;
@@ -290,8 +303,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
                     const int i = i0 + 8 * r, j = n * 8 + j0, last = queries ? i : i - 1;
-                    const float x = s[n][2 * r] * fi[r] * kj.x * ex2(kLog2e * ((hi_i[r] - hj.x) + (lo_i[r] - lj.x)));
-                    const float y = s[n][2 * r + 1] * fi[r] * kj.y * ex2(kLog2e * ((hi_i[r] - hj.y) + (lo_i[r] - lj.y)));
+                    const float x = s[n][2 * r] * fi[r] * kj.x * ex2((hi_i[r] - hj.x) + (lo_i[r] - lj.x));
+                    const float y = s[n][2 * r + 1] * fi[r] * kj.y * ex2((hi_i[r] - hj.y) + (lo_i[r] - lj.y));
                     float2 v = make_float2(j <= last ? x : 0.0f, j + 1 <= last ? y : 0.0f);
                     if (!queries) {
                         *reinterpret_cast<float2 *>(at + D::A + (i * D::AS + j) * 4) = v;
@@ -307,10 +320,10 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             bar_sync(kTeam, FRONT);   // all have read the rows' lengths, which become the rows' factors
             if (w == 1) {
                 const float hi = f[kSumHi * C + lane], lo = f[kSumLo * C + lane], beta = f[kBeta * C + lane];
-                const float reach = ex2(kLog2e * hi) * (1.0f + lo), fk = f[kToEnd * C + lane];
+                const float reach = ex2(hi) * (1.0f + 0.69314718f * lo), fk = f[kToEnd * C + lane];
                 *reinterpret_cast<float2 *>(f + kXy * C + 2 * lane) = make_float2(beta, beta * reach * fk);
                 f[kQReach * C + lane] *= reach;
-                f[kToEnd * C + lane] = fk * ex2(kLog2e * ((f[kSumHi * C + C - 1] - hi) + (f[kSumLo * C + C - 1] - lo)));
+                f[kToEnd * C + lane] = fk * ex2((f[kSumHi * C + C - 1] - hi) + (f[kSumLo * C + C - 1] - lo));
                 if (lane == C - 1) f[kTotal * C] = reach;
             }
             bar_arrive(kFull + slot, ALL);
@@ -338,6 +351,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 const double before = __shfl_up_sync(~0u, sum, m);
                 if (lane >= m) sum += before;
             }
+            sum *= 1.4426950408889634;   // as powers of two
             const float hi = (float)sum, beta = live ? step_of(bv, a.sigmoid) : 0.0f;
             // the slot is free: the four warps have met this one for the chunk before, and waited for it earlier still
             float *f = factors(slot);
@@ -498,18 +512,21 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
         for (int n = 0; n < NC; n++) take(n, sk[n]);
         take(4, yq[0]), take(5, yq[1]);
         // x in the place of S^T k
-        const T *vs = reinterpret_cast<const T *>(smem + slot * D::SLOT + D::V) + lane % 4 * D::TS + rd;   // TS bytes: 2 rows of TS / 2
         float u[NC][4] = {};
         {
             uint32_t xp[3][NC / 2][4];
             float down[2];
+            uint32_t v[2][4];   // values of eight columns and all rows, transposed: a lane's column, two rows a register
+#pragma unroll
+            for (int i = 0; i < 2; i++) ldsm4t(v[i], at + D::V + lane * D::TS + (pair * 16 + i * 8) * 2);
 #pragma unroll
             for (int n = 0; n < NC; n++) {
                 const float4 w = *reinterpret_cast<const float4 *>(f + kXy * C + 2 * (n * 8 + lane % 4 * 2));   // B, .. of two rows
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float v = Storage<T>::to_f(vs[(n * 8 + e % 2) * (D::TS / 2) + e / 2 * 8]);
-                    sk[n][e] = fmaf(e % 2 ? -w.w : -w.y, sk[n][e], (e % 2 ? w.z : w.x) * v);
+                for (int i = 0; i < 2; i++) {
+                    const float2 x = two_of<T>(v[i][n]);
+                    sk[n][2 * i] = fmaf(-w.y, sk[n][2 * i], w.x * x.x);
+                    sk[n][2 * i + 1] = fmaf(-w.w, sk[n][2 * i + 1], w.z * x.y);
                 }
             }
             as_half(sk, xp, down);
