@@ -156,17 +156,17 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool live)
 // parts, 22 bits, as x and T do; products of second f16 parts, below 2^-22, are left out.  What only y needs (S^T q, P u)
 // has two parts, 2^-16 at least, where y keeps 2^-8 or 2^-11.
 //
-// 8192 rows of 32 heads of 128 x 128, bf16, 592 us: 2.3 us a chunk, 128 blocks on as many SMs.  A chunk's chain (S to its
-// parts, S^T k, x, u, S again) is what it costs; the tensor cores are 41 % busy and 39 % of the issue slots taken.  Each of
-// these, taken out alone, saves 90 to 125 us: the rows' loads, the inverse, the products that make A and P, S^T k and q.  What
-// was tried, us: S and u in two f16 parts, keys converted to f16 in the block, 1074 (the conversions bind); four warps for 16
-// columns, 32 keys each, 1430; three slots of rows 747; y finished a chunk later 820; x and T in three bf16 parts 678;
-// products in the order of their sums, each waiting for the one before, 745.  The loops are short because the roles' code has
-// to stay in the instruction cache together: with the inverse's products unrolled, and keys converted, the warps waited 2.6
-// cycles an instruction for their code (1430 us).
+// 8192 rows of 32 heads of 128 x 128, bf16, 499 us: 1.95 us a chunk, 128 blocks on as many SMs.  A chunk's chain (S to its
+// parts, S^T k, x, u, S again) is what it costs: taken out alone, S^T k and q with the states' products save 103 us, the
+// inverse 53, the rows' loads 26, the products that make A and P 18.  The tensor cores are under a half busy, as are the issue
+// slots.  What was tried, us: four warps for 16 columns, 32 keys each, all factors in two f16 parts and keys converted in the block,
+// 1430, two warps so 1074 (the conversions bind); x and T in three bf16 parts 678 where 602 was; products in the order of
+// their sums, each waiting for the one before, 745 for 678; three slots of rows 731; S^T q's products after the meeting 503.
+// The loops are short because the roles' code has to stay in the instruction cache together: with the inverse's products
+// unrolled, and keys converted, the warps waited 2.6 cycles an instruction for their code.
 //
-// Four blocks make the same A, P and T, one for each 32 columns of a head.  A cluster that shares them would save a fifth; its
-// blocks would wait for each other in every chunk.
+// Four blocks make the same A, P and T, one for each 32 columns of a head.  A cluster that shares them would save some of
+// the 97 us above; its blocks would wait for each other in every chunk.
 template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::THREADS, 1) delta_chunk_kernel(const DeltaArgs a) {
     using D = DeltaChunk<DK>;
     using B = __nv_bfloat16;
