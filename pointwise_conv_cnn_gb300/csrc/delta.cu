@@ -9,26 +9,31 @@
 namespace fcm {
 namespace seq {
 
-// Row by row.  A block has 32 of a head's value columns, a thread four of them and every 16th row of the
-// state, in registers.  Both products with the state need its value before the row only,
+// Row by row.  A block has 32 of a head's value columns, a thread four of them and every 16th row of the state, in
+// registers.  Both products with the state need its value before the row only,
 //     u = B (v - e^G S^T k),   S^T q after it = e^G S^T q + (q.k) u,
-// so that a row costs one sum over the block's threads, through shared memory, and one barrier.  Rows come
-// in batches: their norms, products q.k, decays and steps are made once for all columns by a warp a row.
-// VEC: four columns of the state, v and y are read and written at once.
+// so that a row costs one sum over 16 threads.  Rows come in batches: their norms, products q.k, decays
+// and steps are made once for all columns by a warp a row.  VEC: four columns of the state, v and y are read and
+// written at once.
+// LONG (prompts): the 16 threads are a warp's, so that no row waits at a barrier, and the next batch is on its
+// way while one is computed.  For single tokens they are a block's, whose warps then read and write the state's rows in
+// pieces of 128 bytes instead of 32 (128 sequences of 32 heads 95 us, 113 as for prompts), with registers for six
+// blocks an SM.
 //
-// Single tokens are bound by their states' way in and out: 128 sequences of 32 heads of 128 x 128 move 540 MB in 100 us, 5.4
-// TB/s, 0.80 of a plain copy's rate; one sequence of 16 heads takes 3.6 us, a launch and a chain of loads.  Prompts in
-// 32 bits, and what the chunks do not take, cost 0.65 us a row, the latency of a row's sums: 777 x 8 heads 506 us.
-template <typename T, int RK, bool VEC>
-__global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const DeltaArgs a) {
-    constexpr int TB = 8, DK = 16 * RK, DV = kDeltaCols;
+// Single tokens are bound by their states' way in and out: 128 sequences of 32 heads of 128 x 128 move 540 MB in 95 us, 5.7
+// TB/s, 0.84 of a plain copy's rate; one sequence of 16 heads takes 3.6 us, a launch and a chain of loads.  Prompts in
+// 32 bits, and what the chunks do not take, cost the latency of a row's sums: 777 x 8 heads of 128 x 128 317 us.
+template <typename T, int RK, bool VEC, bool LONG>
+__global__ void __launch_bounds__(128, LONG ? 3 : RK <= 8 ? 6 : 3) delta_row_kernel(const DeltaArgs a) {
+    constexpr int TB = 8, DK = 16 * RK, DV = kDeltaCols, KN = TB * DK / 128, VN = TB * DV / 128;
     __shared__ float qs[TB][DK], ks[TB][DK], vs[TB][DV];
     __shared__ float4 row[TB];    // e^G, B, 1 / |k|, scale / |q|
     __shared__ float prod[TB];    // q.k
-    __shared__ float4 red[2][4][8][2];
+    __shared__ float4 red[LONG ? 1 : 2][4][8][2];
     tc::pdl_wait();
     tc::pdl_launch_dependents();
-    const int tx = threadIdx.x % 8, ty = threadIdx.x / 8, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, tx = LONG ? 2 * warp + lane % 2 : threadIdx.x % 8,
+              ty = LONG ? lane / 2 : threadIdx.x / 8;
     const int slice = blockIdx.x % a.slices, rest = blockIdx.x / a.slices;
     const int h = rest % a.heads, q = rest / a.heads, g = h / a.per_key;
     long long t0;
@@ -55,22 +60,58 @@ __global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const D
     const T *vp = static_cast<const T *>(a.vp) + (size_t)h * a.dv + d0;
     T *y = static_cast<T *>(a.y) + (size_t)h * a.dv + d;
     const float av = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+    // element i of a batch's keys, queries (row i / DK) or values (i / DV), zeros past the rows and columns
+    auto element = [&](const T *p, long long ld, int b0, int i, int width, int columns) {
+        const int j = i / width, e = i % width;
+        return b0 + j < len && e < columns ? p[(t0 + b0 + j) * ld + e] : Storage<T>::from_f(0.0f);
+    };
+    T kn[LONG ? KN : 1], qn[LONG ? KN : 1], vn[LONG ? VN : 1], dtn[2], bn[2];
+    auto scalars = [&](int b0) {   // of this warp's rows: warp, warp + 4
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const bool live = b0 + warp + 4 * i < len;
+            const long long t = live ? t0 + b0 + warp + 4 * i : t0;
+            dtn[i] = live ? static_cast<const T *>(a.dt)[t * a.ld_dt + h] : Storage<T>::from_f(0.0f);
+            bn[i] = live ? static_cast<const T *>(a.b)[t * a.ld_b + h] : Storage<T>::from_f(0.0f);
+        }
+    };
+    auto fetch = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < KN; i++) {
+            kn[i] = element(kp, a.ld_k, b0, threadIdx.x + 128 * i, DK, a.dk);
+            qn[i] = element(qp, a.ld_q, b0, threadIdx.x + 128 * i, DK, a.dk);
+        }
+#pragma unroll
+        for (int i = 0; i < VN; i++) vn[i] = element(vp, a.ld_v, b0, threadIdx.x + 128 * i, DV, a.dv - d0);
+    };
+    if (len > 0) {
+        scalars(0);
+        if constexpr (LONG) fetch(0);
+    }
     for (int b0 = 0, n; b0 < len; b0 += n) {
         n = min(TB, len - b0);
-        const long long t = t0 + b0;
-        for (int i = threadIdx.x; i < n * DK; i += 128) {
-            const int j = i / DK, e = i % DK;
-            const bool in = e < a.dk;
-            qs[j][e] = in ? Storage<T>::to_f(qp[(t + j) * a.ld_q + e]) : 0.0f;
-            ks[j][e] = in ? Storage<T>::to_f(kp[(t + j) * a.ld_k + e]) : 0.0f;
-        }
-        for (int i = threadIdx.x; i < n * DV; i += 128) {
-            const int j = i / DV, e = i % DV;
-            vs[j][e] = d0 + e < a.dv ? Storage<T>::to_f(vp[(t + j) * a.ld_v + e]) : 0.0f;
+        if constexpr (LONG) {
+#pragma unroll
+            for (int i = 0; i < KN; i++) {
+                (&ks[0][0])[threadIdx.x + 128 * i] = Storage<T>::to_f(kn[i]);
+                (&qs[0][0])[threadIdx.x + 128 * i] = Storage<T>::to_f(qn[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < VN; i++) (&vs[0][0])[threadIdx.x + 128 * i] = Storage<T>::to_f(vn[i]);
+        } else {
+            for (int i = threadIdx.x; i < n * DK; i += 128) {
+                (&ks[0][0])[i] = Storage<T>::to_f(element(kp, a.ld_k, b0, i, DK, a.dk));
+                (&qs[0][0])[i] = Storage<T>::to_f(element(qp, a.ld_q, b0, i, DK, a.dk));
+            }
+            for (int i = threadIdx.x; i < n * DV; i += 128) (&vs[0][0])[i] = Storage<T>::to_f(element(vp, a.ld_v, b0, i, DV, a.dv - d0));
         }
         __syncthreads();
-        for (int j = warp; j < n; j += 4) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int j = warp + 4 * i;
+            if (j >= n) break;
             float qq = 0.0f, kk = 0.0f, qk = 0.0f;
+#pragma unroll
             for (int e = lane; e < DK; e += 32) {
                 const float x = qs[j][e], z = ks[j][e];
                 qq = fmaf(x, x, qq), kk = fmaf(z, z, kk), qk = fmaf(x, z, qk);
@@ -80,15 +121,17 @@ __global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const D
                 qq += __shfl_xor_sync(~0u, qq, m), kk += __shfl_xor_sync(~0u, kk, m), qk += __shfl_xor_sync(~0u, qk, m);
             }
             if (lane == 0) {
-                const float dt = Storage<T>::to_f(static_cast<const T *>(a.dt)[(t + j) * a.ld_dt + h]);
-                const float bv = Storage<T>::to_f(static_cast<const T *>(a.b)[(t + j) * a.ld_b + h]);
-                row[j] = make_float4(expf(log_decay(dt + bias, av, a.softplus)), step_of(bv, a.sigmoid),
-                                     a.normalize ? rsqrtf(kk + kDeltaEps) : 1.0f,
+                row[j] = make_float4(expf(log_decay(Storage<T>::to_f(dtn[i]) + bias, av, a.softplus)),
+                                     step_of(Storage<T>::to_f(bn[i]), a.sigmoid), a.normalize ? rsqrtf(kk + kDeltaEps) : 1.0f,
                                      a.normalize ? a.scale * rsqrtf(qq + kDeltaEps) : a.scale);
                 prod[j] = qk;
             }
         }
         __syncthreads();
+        if (len - b0 > TB) {
+            scalars(b0 + TB);
+            if constexpr (LONG) fetch(b0 + TB);
+        }
         for (int j = 0; j < n; j++) {
             float pk[4] = {}, pq[4] = {}, kr[RK];
 #pragma unroll
@@ -99,25 +142,29 @@ __global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const D
                 for (int e = 0; e < 4; e++) pk[e] = fmaf(kr[r], s[r][e], pk[e]), pq[e] = fmaf(qr, s[r][e], pq[e]);
             }
 #pragma unroll
-            for (int m = 8; m < 32; m <<= 1)
+            for (int m = LONG ? 2 : 8; m < 32; m <<= 1)
 #pragma unroll
                 for (int e = 0; e < 4; e++) pk[e] += __shfl_xor_sync(~0u, pk[e], m), pq[e] += __shfl_xor_sync(~0u, pq[e], m);
-            if (lane < 8) {
-                red[j & 1][warp][tx][0] = make_float4(pk[0], pk[1], pk[2], pk[3]);
-                red[j & 1][warp][tx][1] = make_float4(pq[0], pq[1], pq[2], pq[3]);
-            }
-            __syncthreads();
-            float4 sk = red[j & 1][0][tx][0], sq = red[j & 1][0][tx][1];
+            if constexpr (!LONG) {
+                auto &sums = red[j & 1];
+                if (lane < 8) {
+                    sums[warp][tx][0] = make_float4(pk[0], pk[1], pk[2], pk[3]);
+                    sums[warp][tx][1] = make_float4(pq[0], pq[1], pq[2], pq[3]);
+                }
+                __syncthreads();
 #pragma unroll
-            for (int w = 1; w < 4; w++) {
-                const float4 x = red[j & 1][w][tx][0], z = red[j & 1][w][tx][1];
-                sk.x += x.x, sk.y += x.y, sk.z += x.z, sk.w += x.w;
-                sq.x += z.x, sq.y += z.y, sq.z += z.z, sq.w += z.w;
+                for (int e = 0; e < 4; e++) pk[e] = pq[e] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    const float4 x = sums[w][tx][0], z = sums[w][tx][1];
+                    pk[0] += x.x, pk[1] += x.y, pk[2] += x.z, pk[3] += x.w;
+                    pq[0] += z.x, pq[1] += z.y, pq[2] += z.z, pq[3] += z.w;
+                }
             }
             const float4 f = row[j], v = *reinterpret_cast<const float4 *>(&vs[j][4 * tx]);
             const float fk = f.x * f.z;
-            const float u[4] = {f.y * fmaf(-fk, sk.x, v.x), f.y * fmaf(-fk, sk.y, v.y), f.y * fmaf(-fk, sk.z, v.z),
-                                f.y * fmaf(-fk, sk.w, v.w)};
+            const float u[4] = {f.y * fmaf(-fk, pk[0], v.x), f.y * fmaf(-fk, pk[1], v.y), f.y * fmaf(-fk, pk[2], v.z),
+                                f.y * fmaf(-fk, pk[3], v.w)};
 #pragma unroll
             for (int r = 0; r < RK; r++) {
                 const float k = f.z * kr[r];
@@ -126,9 +173,10 @@ __global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const D
             }
             if (ty == 0) {
                 const float qk = f.z * prod[j];
-                const float o[4] = {f.w * fmaf(qk, u[0], f.x * sq.x), f.w * fmaf(qk, u[1], f.x * sq.y),
-                                    f.w * fmaf(qk, u[2], f.x * sq.z), f.w * fmaf(qk, u[3], f.x * sq.w)};
-                T *to = y + (t + j) * a.ld_y;
+                float o[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) o[e] = f.w * fmaf(qk, u[e], f.x * pq[e]);
+                T *to = y + (t0 + b0 + j) * a.ld_y;
                 if (VEC) {
                     if (d < a.dv) {
                         Vec<T, 4> v4;
@@ -163,8 +211,11 @@ __global__ void __launch_bounds__(128, RK <= 8 ? 6 : 3) delta_row_kernel(const D
 
 // Longest sequence's rows from which prompts go in chunks.  Where blocks are few chunks are ahead from 6 rows on, where
 // they are many from 14.  Measured, us row by row and in chunks, heads of 128 x 128, bf16: 1 sequence of 32 heads, 4, 6, 8, 12
-// rows 5.1, 6.9, 7.8, 10.8 and 6.2; 64 of 8 heads 27, 37, 43, 58 and 68; 1 of 32 heads, 40 rows 30.7 and 8.1.
+// rows 5.0, 6.4, 7.4, 7.5 and 6.2; 64 of 8 heads 27, 34, 40, 54 and 68.
 constexpr int kChunkedFrom = 16;
+// ... and from which the row kernel is the prompts': 64 sequences of 8 heads, 2, 4, 8 rows 21.4, 27.0, 40.2 us, as single
+// tokens 20.3, 28.2, 44.7.
+constexpr int kManyFrom = 3;
 
 template <typename T, int DK> static cudaError_t run_chunks(const DeltaArgs &a, dim3 grid, cudaStream_t st) {
     static std::atomic<unsigned long long> attr{0};
@@ -189,7 +240,12 @@ template <typename T> static cudaError_t run_delta(DeltaArgs a, cudaStream_t st)
         if (a.q.max_len >= kChunkedFrom && a.dk <= 128)
             return a.dk <= 64 ? run_chunks<T, 64>(a, grid, st) : run_chunks<T, 128>(a, grid, st);
     }
-#define ROWS(rk) launch(vec ? delta_row_kernel<T, rk, true> : delta_row_kernel<T, rk, false>, grid, 128, 0, st, a)
+    auto rows = [&](void (*one)(DeltaArgs), void (*one_vec)(DeltaArgs), void (*many)(DeltaArgs), void (*many_vec)(DeltaArgs)) {
+        return launch(a.q.max_len >= kManyFrom ? (vec ? many_vec : many) : (vec ? one_vec : one), grid, 128, 0, st, a);
+    };
+#define ROWS(rk) \
+    rows(delta_row_kernel<T, rk, false, false>, delta_row_kernel<T, rk, true, false>, delta_row_kernel<T, rk, false, true>, \
+         delta_row_kernel<T, rk, true, true>)
     return a.dk <= 64 ? ROWS(4) : a.dk <= 128 ? ROWS(8) : ROWS(16);
 #undef ROWS
 }
