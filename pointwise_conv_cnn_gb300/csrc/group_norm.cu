@@ -83,10 +83,10 @@ template <typename T, int V, int LPG, int NV, int ROWS>
 __global__ void __launch_bounds__(256) norm_rows_kernel(const NormArgs a) {
     tc::pdl_wait();
     tc::pdl_launch_dependents();
-    const long long unit = ((long long)blockIdx.x * 256 + threadIdx.x) / LPG;
+    const unsigned unit = blockIdx.x * (256u / LPG) + threadIdx.x / LPG;   // groups of ROWS rows: 2^31 at most, and a block's
     const int lane = threadIdx.x % LPG;
-    const int g = (int)(unit % a.groups);
-    const long long r0 = unit / a.groups * ROWS;   // past the last row: the lanes go along, and store nothing
+    const int g = (int)(unit % (unsigned)a.groups);
+    const long long r0 = (long long)(unit / (unsigned)a.groups) * ROWS;   // past the last row: the lanes go along, and store nothing
     float x[ROWS][NV][V];
     bool in[NV];
     int d[NV];

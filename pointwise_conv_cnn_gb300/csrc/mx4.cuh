@@ -1,6 +1,7 @@
 // mx4.cuh -- the values of microscaled 4-bit floating point.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 namespace fcm {
@@ -14,10 +15,11 @@ __device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
     return r;
 }
 
-// The value of the code in the low four bits: sign, two bits of exponent, one of mantissa.  Put into a
-// float's bits they stand for value * 2^-126 (the subnormal step 0.5 included).
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-    return __uint_as_float((code & 8u) << 28 | (code & 7u) << 22) * 0x1p126f;
+// The values of the two codes in the low byte, that of the low four bits first: exact in f16.
+__device__ __forceinline__ float2 e2m1_values(uint32_t codes) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(codes));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
 // 2^(code - 127), NaN for 255.
