@@ -571,8 +571,8 @@ template <typename T, int V> static cudaError_t run_maps(NormArgs a, bool may_sh
         else break;
     }
     // Whether clusters share samples instead, which costs two launches and the joining of their sums, some 30 us.  A block
-    // takes 1.1 ns a vector and so does an SM (measured from 40000 x 66 in pairs of channels, 204 us by 8 blocks, to 512 x
-    // 512 x 128, 62 shared).  What the blocks' shared memory does not keep is read again, at half the speed: a sample of
+    // takes 1.1 ns a vector and so does an SM (measured from 40000 x 66 in pairs of channels, 204 us by 8 blocks and 16 shared,
+    // to 512 x 512 x 128, 55 shared).  What the blocks' shared memory does not keep is read again, at half the speed: a sample of
     // 40000 x 128 21 us and 33 shared, 90000 x 128 53 and 39; 32 samples of 8192 x 128 106 and 75, 16 32 and 51.
     const double sample = (double)a.pixels * a.c, vectors = sample / V, blocks = (double)nb * cl, bytes = sample * sizeof(T);
     if (may_share && (1.1e-3 * vectors / blocks > 35.0 + 1.1e-3 * vectors * a.n / sms || bytes > 16e6 ||

@@ -179,7 +179,7 @@ template <int NT> __global__ void __launch_bounds__(256, 2) mx4_matmul_kernel(co
     const uint32_t at_a = base, at_b = at_a + S::ST * S::A, at_sf = at_b + S::ST * S::B, bars = at_sf + S::ST * 2 * S::SF;
     const uint32_t full = bars, sf_full = bars + 8 * S::ST, empty = bars + 16 * S::ST, done = bars + 24 * S::ST;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const unsigned tile = blockIdx.x / a.split, rank = blockIdx.x % a.split, tiles_m = (unsigned)(a.m + NT - 1) / NT;
+    const unsigned tile = blockIdx.x / a.split, rank = blockIdx.x % a.split, tiles_m = ((unsigned)a.m + NT - 1) / NT;
     const int m0 = (int)(tile % tiles_m) * NT, o0 = (int)(tile / tiles_m) * 128;
     const int c0 = (int)((long long)a.chunks * rank / a.split), c1 = (int)((long long)a.chunks * (rank + 1) / a.split);
     const int stages = min(2 * c1, (a.groups + 7) / 8) - 2 * c0;   // of 8 codes
@@ -370,7 +370,7 @@ static cudaError_t run_mx4(Mx4MatmulArgs &a, const void *wq, const void *xq, int
         if (e != cudaSuccess) return e;
         attr.store(ctx, std::memory_order_relaxed);
     }
-    const long long tiles = (long long)((a.m + NT - 1) / NT) * ((a.out + 127) / 128);
+    const long long tiles = ((a.m + NT - 1ll) / NT) * ((a.out + 127ll) / 128);
     // Blocks that share the inputs of a tile, where the tiles leave SMs without a block.  More than four, and for 128
     // tokens a second block an SM, cost more than they bring.  Measured, us without sharing, with two, four and eight: 16
     // tokens, 4096 x 4096 (32 tiles) 9.2, -, 6.5, 8.4; 300 tokens, 1000 x 8192 (24) 19.7, -, 11.8, 12.7; 16 tokens, 8192 x
@@ -412,7 +412,7 @@ extern "C" fcm_status fcm_mx4_matmul(const fcm_mx4_matmul_desc *desc, const void
         return fcm_fail(FCM_ERR_INVALID_ARG, "xq or xs and y overlap");
     int sms;
     if ((st = seq::current_device(&sms)) != FCM_OK) return st;
-    const long long most = (((long long)d.m + 15) / 16) * ((d.out + 127) / 128);   // blocks of the smallest tiles
+    const long long most = ((d.m + 15ll) / 16) * ((d.out + 127ll) / 128);   // blocks of the smallest tiles
     if (most * 8 > 0x7FFFFFFFLL) return fcm_fail(FCM_ERR_UNSUPPORTED, "m %d, out %d: above 2^31 - 1 blocks", d.m, d.out);
     seq::Mx4MatmulArgs a = {};
     a.ws = static_cast<const uint8_t *>(ws), a.xs = static_cast<const uint8_t *>(xs), a.s = s, a.b = b, a.y = y;
