@@ -286,8 +286,8 @@ template <int N> __device__ __forceinline__ void join_sums(float &n, float &m, f
 // about the mean: a thread's channels of a group, threads in shared memory, blocks through distributed shared memory,
 // in one order always.
 constexpr int kMapThreads = 256;
-template <typename T, int V, bool GATE> __global__ void __launch_bounds__(kMapThreads, 2) norm_maps_kernel(const NormArgs a) {
-    constexpr int U = 4, RING = 8, nt = kMapThreads, warps = nt / 32;
+template <typename T, int V, bool GATE, int BLOCKS> __global__ void __launch_bounds__(kMapThreads, BLOCKS) norm_maps_kernel(const NormArgs a) {
+    constexpr int U = BLOCKS == 2 ? 4 : 2, RING = 8, nt = kMapThreads, warps = nt / 32;
     constexpr int BYTES = V * sizeof(T);
     constexpr bool ASYNC = BYTES >= 4;   // single 16-bit channels go through registers
     extern __shared__ __align__(16) unsigned char smem[];
@@ -514,18 +514,19 @@ template <int V> static size_t maps_fixed(int groups_of_block) {
     return (size_t)kMapThreads * V * 8 + (size_t)(5 * groups_of_block + 3) / 4 * 16;
 }
 
-template <typename T, int V>
+template <typename T, int V, int BLOCKS>
 static cudaError_t launch_maps(const NormArgs &a, long long blocks, size_t smem, int cl, cudaStream_t st) {
     static std::atomic<unsigned long long> attr{0};
     const unsigned long long ctx = fcm_current_ctx_id();
+    void (*const plain)(NormArgs) = norm_maps_kernel<T, V, false, BLOCKS>;
+    void (*const gated)(NormArgs) = norm_maps_kernel<T, V, true, BLOCKS>;
     if (ctx == 0 || attr.load(std::memory_order_relaxed) != ctx) {
-        cudaError_t e = cudaFuncSetAttribute(norm_maps_kernel<T, V, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(norm_maps_kernel<T, V, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        cudaError_t e = cudaFuncSetAttribute(plain, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(gated, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
         attr.store(ctx, std::memory_order_relaxed);
     }
-    return launch(a.z ? norm_maps_kernel<T, V, true> : norm_maps_kernel<T, V, false>, dim3((unsigned)blocks), kMapThreads, smem, st, a, cl);
+    return launch(a.z ? gated : plain, dim3((unsigned)blocks), kMapThreads, smem, st, a, cl);
 }
 
 // Samples too large for a cluster: clusters share one, and leave their groups' sums in y's first pixels, which are written
@@ -543,7 +544,7 @@ template <typename T, int V> static cudaError_t run_shared(NormArgs a, int sms, 
     a.parts = parts < 1 ? 1 : parts > kMostParts ? kMostParts : parts;
     a.nb = 1;
     a.ppc = (a.pixels + a.parts * CL - 1) / (a.parts * CL);
-    cudaError_t e = launch_maps<T, V>(a, (long long)a.n * a.parts * CL, fixed + (a.async ? ring : 0), CL, st);
+    cudaError_t e = launch_maps<T, V, 2>(a, (long long)a.n * a.parts * CL, fixed + (a.async ? ring : 0), CL, st);
     if (e != cudaSuccess) return e;
     a.skip = (32 + 12ll * a.parts * a.groups + row - 1) / row;
     // as many blocks as are on the SMs at once: each joins the sums first
@@ -588,7 +589,13 @@ template <typename T, int V> static cudaError_t run_maps(NormArgs a, bool may_sh
     a.async = room >= rounds || room >= 8;
     a.hold = (int)((rounds < room ? rounds : room) * round);
     const size_t smem = fixed + a.hold * row;
-    return launch_maps<T, V>(a, (long long)a.n * a.nb * cl, smem, cl, st);
+    // Three blocks an SM, with fewer registers, where there are blocks for more than two rounds of two and room for three: us with
+    // two and three, 64 x 56 x 56 x 128 (1024 blocks) 44.7 and 38.5, 32 x (512) 26.0 and 28.3, 16 x 18.8 and 20.4;
+    // 64 x 32 x 32 x 320 50.9 and 43.1, gated 64 x 56 x 56 x 128 in bf16 78.1 and 74.9 (seven registers of it spill).
+    const long long all = (long long)a.n * a.nb * cl;
+    if constexpr (V * sizeof(T) == 16)
+        if (all > 4ll * sms && smem <= 74 * 1024) return launch_maps<T, V, 3>(a, all, smem, cl, st);
+    return launch_maps<T, V, 2>(a, all, smem, cl, st);
 }
 
 template <typename T, int V, int LPG, int NV, int ROWS> static cudaError_t rows_kernel(const NormArgs &a, cudaStream_t st) {
