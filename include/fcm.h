@@ -448,8 +448,8 @@ FCM_API fcm_status fcm_w4_matvec(const fcm_w4_desc *desc, const void *x, const v
  * heads.  Any dt and a are taken, infinite ones too: e^G is 0 below G = -104, and the state grows where G > 0.
  * Prompts (16-bit types, dk up to 128, a longest sequence of 16 rows or more) go through in chunks of 32 rows, whose
  * products meet each other before any sum: a NaN or an infinity among a head's rows, states or decays may therefore make
- * any row of that head and sequence from the chunk's first on NaN, as may factors whose product over a chunk's rows leaves a float's
- * range, or keys that are not normalised where the rule multiplies what it was told by more than 65504 within 32 rows. */
+ * any row of that head and sequence from the chunk's first on NaN, as may rows that multiply what they are told by more than a
+ * float's range within 32 of them, by factors e^G or by keys that are not normalised. */
 typedef struct fcm_delta_desc {
     fcm_seqs seqs;
     int heads, key_heads, dk, dv, dtype, softplus, sigmoid, normalize;

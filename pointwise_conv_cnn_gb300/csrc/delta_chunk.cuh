@@ -20,10 +20,10 @@ template <int DK> struct DeltaChunk {
     static constexpr int THREADS = 32 * (STATE + FRONT + 2);
     static constexpr int SLOTS = 4, AHEAD = 2;        // chunks in flight, chunks whose rows are asked for ahead
     static constexpr int KS = 2 * DK + 16;            // bytes of a row of keys: eight rows in different banks
-    static constexpr int TS = 80;                     // of T's and the rows' products' 16-bit parts, and of values
+    static constexpr int TS = 80;                     // of T's three and the rows' products' two 16-bit parts, and of values
     static constexpr int AS = 36;                     // floats of a row of A, and of T on its way
     // a slot's parts, bytes
-    static constexpr int Q = C * KS, V = 2 * C * KS, TP = V + C * TS, PP = TP + 2 * C * TS, A = PP + 2 * C * TS,
+    static constexpr int Q = C * KS, V = 2 * C * KS, TP = V + C * TS, PP = TP + 3 * C * TS, A = PP + 2 * C * TS,
                          SC = A + C * AS * 4, SLOT = SC + 8 * C * 4;
     static constexpr int XCH = 2 * 2 * DS * 8 * 512;   // sums on their way between warps: [turn][16 columns][warp][16 bytes][lane]
     static constexpr int TMP = C * AS * 4;             // T's diagonal blocks
@@ -153,8 +153,12 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool live)
 //
 // Rounding: keys and queries are used as they are, and their lengths, decays and steps applied to sums in 32 bits.  S and
 // the decayed u enter products with bf16 keys in three bf16 parts, which hold all 24 bits, and with f16 keys in two f16
-// parts, 22 bits, as x and T do; products of second f16 parts, below 2^-22, are left out.  What only y needs (S^T q, P u)
-// has two parts, 2^-16 at least, where y keeps 2^-8 or 2^-11.
+// parts, 22 bits, under a power of two for each column; products of second f16 parts, below 2^-22, are left out.  T and x are in three
+// bf16 parts for either type (products of parts below 2^-22 are left out): T holds e^(c_i - c_j), x the rows' values beside what the
+// state recalls, so that in a chunk where states grow or fall by much their numbers lie further apart than f16 reaches.
+// (In two f16 parts T was infinite from 65504 on, 23 rows of G = 0.5, and had lost what it says of a state 2^14 times as large
+// as the values; 503 us where these take 552.)  What only y needs (S^T q, P u) has two parts, 2^-16 at least, where y keeps
+// 2^-8 or 2^-11.
 //
 // 8192 rows of 32 heads of 128 x 128, bf16, 499 us: 1.95 us a chunk, 128 blocks on as many SMs.  A chunk's chain (S to its
 // parts, S^T k, x, u, S again) is what it costs: taken out alone, S^T k and q with the states' products save 103 us, the
@@ -368,12 +372,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             const int slot = c % D::SLOTS;
             bar_sync(kFull + slot, ALL);
             const float *A = reinterpret_cast<const float *>(smem + slot * D::SLOT + D::A);
-            __half *to = reinterpret_cast<__half *>(smem + slot * D::SLOT + D::TP);
-            auto put = [&](int i, int col, float v) {   // in two parts
-                const __half hi = __float2half_rn(v);
-                to[i * (D::TS / 2) + col] = hi;
-                to[(C + i) * (D::TS / 2) + col] = __float2half_rn(v - __half2float(hi));
-            };
+            const uint32_t to = base + slot * D::SLOT + D::TP;   // T's parts transposed: a lane's column lies together
             float t[16];
             const float *Ad = A + 16 * half * (D::AS + 1);
 #pragma unroll
@@ -393,42 +392,52 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             __syncwarp();
             // Below them -T22 A21 T11, as the transposed products T11^T A21^T and that times T22^T, whose right factors lie
             // as they are needed and whose sums are the next left factors.
-            // None is scaled: a product over 65504 is no number any more (as the rule multiplies keys that are not
-            // normalised, within 32 rows).
             float sum[2][4];
-            uint32_t left[2][4];
-            auto factor = [&] {
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    split2(sum[e / 2][e % 2 * 2], sum[e / 2][e % 2 * 2 + 1], left[0][e], left[1][e]);
-                }
-            };
+            uint32_t left[3][1][4];
             auto times = [&](const float *from) {   // left factors by the rows of `from`
 #pragma unroll
                 for (int n = 0; n < 2; n++) {
                     const float *p = from + (n * 8 + lane / 4) * D::AS + lane % 4 * 2;
-                    const float2 lo = *reinterpret_cast<const float2 *>(p), hi = *reinterpret_cast<const float2 *>(p + 8);
-                    uint32_t b0[2], b1[2];
-                    split2(lo.x, lo.y, b0[0], b0[1]), split2(hi.x, hi.y, b1[0], b1[1]);
-                    float s[4] = {};
-                    mma16<__half>(s, left[0], b0[1], b1[1]);
-                    mma16<__half>(s, left[1], b0[0], b1[0]);
-                    mma16<__half>(s, left[0], b0[0], b1[0]);
+                    float2 lo = *reinterpret_cast<const float2 *>(p), hi = *reinterpret_cast<const float2 *>(p + 8);
+                    uint32_t b0[3], b1[3];
 #pragma unroll
-                    for (int e = 0; e < 4; e++) sum[n][e] = s[e];
+                    for (int m = 0; m < 3; m++) cut(lo.x, lo.y, b0[m]), cut(hi.x, hi.y, b1[m]);
+                    float s[4] = {}, r[4] = {};   // two sums: half the chain
+                    mma16<B>(r, left[2][0], b0[0], b1[0]);
+                    mma16<B>(s, left[1][0], b0[0], b1[0]);
+                    mma16<B>(r, left[1][0], b0[1], b1[1]);
+                    mma16<B>(s, left[0][0], b0[1], b1[1]);
+                    mma16<B>(r, left[0][0], b0[2], b1[2]);
+                    mma16<B>(s, left[0][0], b0[0], b1[0]);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) sum[n][e] = s[e] + r[e];
                 }
             };
 #pragma unroll
             for (int e = 0; e < 8; e++)   // tile e / 4 of the left factor: inner places (rows of T11) 8 (e / 4) ..
                 sum[e / 4][e % 4] = own[(lane % 4 * 2 + e % 2 + e / 4 * 8) * D::AS + lane / 4 + e / 2 % 2 * 8];
-            factor();
+            as_bf16<3>(sum, left);
             times(A + 16 * D::AS);
-            factor();
+            as_bf16<3>(sum, left);
             times(own + 16 * (D::AS + 1));
+            uint32_t p[3][8];
 #pragma unroll
-            for (int i = 0; i < 16; i++) put(16 * half + i, 16 * half + j, t[i]);
+            for (int i = 0; i < 8; i++) {
+                float x = t[2 * i], y = t[2 * i + 1];
 #pragma unroll
-            for (int e = 0; e < 8; e++) put(16 + e / 4 * 8 + lane % 4 * 2 + e % 2, lane / 4 + e / 2 % 2 * 8, -sum[e / 4][e % 4]);
+                for (int m = 0; m < 3; m++) cut(x, y, p[m][i]);
+            }
+            as_bf16<3>(sum, left);
+#pragma unroll
+            for (int m = 0; m < 3; m++) {
+                const uint32_t at = to + m * C * D::TS, diagonal = at + lane * D::TS + half * 32;
+                tc::sts128(diagonal, p[m][0], p[m][1], p[m][2], p[m][3]);
+                tc::sts128(diagonal + 16, p[m][4], p[m][5], p[m][6], p[m][7]);
+#pragma unroll
+                for (int e = 0; e < 4; e++)   // the block below, less its sign: rows 8 (e / 2) .., columns 8 (e % 2) ..
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (lane / 4 + e % 2 * 8) * D::TS + 32 + e / 2 * 16 + lane % 4 * 4),
+                                 "r"(left[m][0][e] ^ 0x80008000u) : "memory");
+            }
             __syncwarp();
             bar_arrive(kInv + slot, STATE + 32);
         }
@@ -515,7 +524,6 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
         float u[NC][4] = {};
         {
             uint32_t xp[3][NC / 2][4];
-            float down[2];
             uint32_t v[2][4];   // values of eight columns and all rows, transposed: a lane's column, two rows a register
 #pragma unroll
             for (int i = 0; i < 2; i++) ldsm4t(v[i], at + D::V + lane * D::TS + (pair * 16 + i * 8) * 2);
@@ -529,24 +537,20 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                     sk[n][2 * i + 1] = fmaf(-w.w, sk[n][2 * i + 1], w.z * x.y);
                 }
             }
-            as_half(sk, xp, down);
+            as_bf16<3>(sk, xp);
             bar_sync(kInv + slot, STATE + 32);
 #pragma unroll
-            for (int m = 1; m >= 0; m--) {   // rows n * 8 .. of T reach columns 0 .. n * 8 + 7
+            for (int m = 2; m >= 0; m--) {   // rows n * 8 .. of T reach columns 0 .. n * 8 + 7
                 uint32_t b[NC][4];
 #pragma unroll
-                for (int n = 0; n < NC; n++) ldsm4(b[n], at + D::TP + m * C * D::TS + (n * 8 + lane % 8) * D::TS + lane / 8 * 16);
+                for (int n = 0; n < NC; n++) ldsm4t(b[n], at + D::TP + m * C * D::TS + lane * D::TS + n * 16);
 #pragma unroll
-                for (int l = 1 - m; l >= 0; l--)
+                for (int l = 2 - m; l >= 0; l--)
 #pragma unroll
                     for (int kk = 0; kk < NC / 2; kk++)
 #pragma unroll
-                        for (int n = 2 * kk; n < NC; n++) mma16<__half>(u[n], xp[l][kk], b[n][2 * kk], b[n][2 * kk + 1]);
+                        for (int n = 2 * kk; n < NC; n++) mma16<B>(u[n], xp[l][kk], b[n][2 * kk], b[n][2 * kk + 1]);
             }
-#pragma unroll
-            for (int n = 0; n < NC; n++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) u[n][e] *= down[e / 2];
         }
         // the states after the chunk
         const float total = f[kTotal * C];
