@@ -359,13 +359,14 @@ int64_t pixel_rows(const at::Tensor &t, const at::Tensor &x, const char *what) {
     if (t.numel() == 0) return c;
     if (c > 1 && stride.back() != 1)
         refuse(FCM_ERR_INVALID_ARG, what, ": a row's elements must lie together, strides ", shape_of(stride));
-    int64_t ld = c, next = 0;   // next: the stride that the dimension before has to have; 0: any
+    int64_t ld = c, next = 0;   // next: the stride that the dimension before has to have
+    bool any = false;
     for (size_t i = size.size() - 1; i-- > 0;) {
         if (size[i] == 1) continue;
-        if (!next) ld = stride[i];
+        if (!any) ld = stride[i];
         else if (stride[i] != next)
             refuse(FCM_ERR_INVALID_ARG, what, ": rows must all be the same distance apart, strides ", shape_of(stride));
-        next = stride[i] * size[i];
+        next = stride[i] * size[i], any = true;
     }
     if (ld < c) refuse(FCM_ERR_INVALID_ARG, what, ": rows overlap, strides ", shape_of(stride));
     return ld;
