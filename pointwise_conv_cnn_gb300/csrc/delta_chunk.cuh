@@ -73,11 +73,12 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
     hi = *reinterpret_cast<const uint32_t *>(&h), lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// Two numbers in three parts of bf16, by cutting: the top 16 bits, those of what is left, and the rest, exactly.
-__device__ __forceinline__ void cut(float &a, float &b, uint32_t &part) {
-    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
-    part = __byte_perm(x, y, 0x7632);
-    a -= __uint_as_float(x & 0xFFFF0000u), b -= __uint_as_float(y & 0xFFFF0000u);
+// The next part in bf16 of two numbers: they rounded to 8 bits, and what is left in their place, exactly.  Three parts are all
+// 24 bits of a number, two are off by 2^-17 of it at most.  (Cut instead of rounded, two were off by 2^-15, always towards 0.)
+__device__ __forceinline__ void part_of(float &a, float &b, uint32_t &part) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    part = *reinterpret_cast<const uint32_t *>(&h);
+    a -= __uint_as_float(part << 16), b -= __uint_as_float(part & 0xFFFF0000u);
 }
 // N tiles of 16 x 8 sums as the left factors of the next product, in M parts of bf16.  Tiles 2 i and 2 i + 1 are 16
 // inner places.
@@ -88,7 +89,7 @@ template <int M, int N> __device__ __forceinline__ void as_bf16(const float (&c)
         for (int r = 0; r < 2; r++) {
             float a = c[i][2 * r], b = c[i][2 * r + 1];
 #pragma unroll
-            for (int m = 0; m < M; m++) cut(a, b, part[m][i / 2][i % 2 * 2 + r]);
+            for (int m = 0; m < M; m++) part_of(a, b, part[m][i / 2][i % 2 * 2 + r]);
         }
 }
 
@@ -154,11 +155,11 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool live)
 // Rounding: keys and queries are used as they are, and their lengths, decays and steps applied to sums in 32 bits.  S and
 // the decayed u enter products with bf16 keys in three bf16 parts, which hold all 24 bits, and with f16 keys in two f16
 // parts, 22 bits, under a power of two for each column; products of second f16 parts, below 2^-22, are left out.  T and x are in three
-// bf16 parts for either type (products of parts below 2^-22 are left out): T holds e^(c_i - c_j), x the rows' values beside what the
+// bf16 parts for either type (products of parts below 2^-24 are left out): T holds e^(c_i - c_j), x the rows' values beside what the
 // state recalls, so that in a chunk where states grow or fall by much their numbers lie further apart than f16 reaches.
 // (In two f16 parts T was infinite from 65504 on, 23 rows of G = 0.5, and had lost what it says of a state 2^14 times as large
-// as the values; 503 us where these take 552.)  What only y needs (S^T q, P u) has two parts, 2^-16 at least, where y keeps
-// 2^-8 or 2^-11.
+// as the values; 503 us where these take 535.)  What only y needs has two bf16 parts, and y keeps 2^-9 or 2^-12 of itself:
+// S^T q is off by 2^-17 of its terms, P u, all four products of whose parts are taken, by 2^-16.
 //
 // 8192 rows of 32 heads of 128 x 128, bf16, 499 us: 1.95 us a chunk, 128 blocks on as many SMs.  A chunk's chain (S to its
 // parts, S^T k, x, u, S again) is what it costs: taken out alone, S^T k and q with the states' products save 103 us, the
@@ -314,9 +315,9 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                         *reinterpret_cast<float2 *>(at + D::A + (i * D::AS + j) * 4) = v;
                     } else {
                         uint32_t part;
-                        cut(v.x, v.y, part);
+                        part_of(v.x, v.y, part);
                         *reinterpret_cast<uint32_t *>(at + D::PP + i * D::TS + j * 2) = part;
-                        cut(v.x, v.y, part);
+                        part_of(v.x, v.y, part);
                         *reinterpret_cast<uint32_t *>(at + D::PP + C * D::TS + i * D::TS + j * 2) = part;
                     }
                 }
@@ -401,7 +402,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                     float2 lo = *reinterpret_cast<const float2 *>(p), hi = *reinterpret_cast<const float2 *>(p + 8);
                     uint32_t b0[3], b1[3];
 #pragma unroll
-                    for (int m = 0; m < 3; m++) cut(lo.x, lo.y, b0[m]), cut(hi.x, hi.y, b1[m]);
+                    for (int m = 0; m < 3; m++) part_of(lo.x, lo.y, b0[m]), part_of(hi.x, hi.y, b1[m]);
                     float s[4] = {}, r[4] = {};   // two sums: half the chain
                     mma16<B>(r, left[2][0], b0[0], b1[0]);
                     mma16<B>(s, left[1][0], b0[0], b1[0]);
@@ -425,7 +426,7 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
             for (int i = 0; i < 8; i++) {
                 float x = t[2 * i], y = t[2 * i + 1];
 #pragma unroll
-                for (int m = 0; m < 3; m++) cut(x, y, p[m][i]);
+                for (int m = 0; m < 3; m++) part_of(x, y, p[m][i]);
             }
             as_bf16<3>(sum, left);
 #pragma unroll
@@ -603,9 +604,8 @@ template <typename T, int DK> __global__ void __launch_bounds__(DeltaChunk<DK>::
                 ldsm4(b[1], p + C * D::TS);
 #pragma unroll
                 for (int kk = 0; kk <= i; kk++) {
-                    mma16<B>(w, up[0][kk], b[0][2 * kk], b[0][2 * kk + 1]);
-                    mma16<B>(w, up[0][kk], b[1][2 * kk], b[1][2 * kk + 1]);
-                    mma16<B>(w, up[1][kk], b[0][2 * kk], b[0][2 * kk + 1]);
+#pragma unroll
+                    for (int m = 3; m >= 0; m--) mma16<B>(w, up[m % 2][kk], b[m / 2][2 * kk], b[m / 2][2 * kk + 1]);
                 }
                 const int r = n * 8 + lane % 4 * 2, live = len - c * C - r;   // rows r and r + 1
                 const float2 reach = *reinterpret_cast<const float2 *>(f + kQReach * C + r);
