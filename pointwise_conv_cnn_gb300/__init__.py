@@ -574,7 +574,8 @@ def gated_delta(q, k, v, dt, a, b, y, dt_bias=None, softplus: bool = True, sigmo
     q, k: [sequences, length, key heads, dk], or [tokens, key heads, dk] with seq_start; v, y: the same
     leading shape with [heads, dv] behind it; dt, b: with [heads]; all in q's dtype, rows may be column
     blocks of wider tensors.  a, dt_bias: float32 [heads].  scale: of the queries (default dk ** -0.5).
-    state_in, state_out: float32 [slots, heads, dk, dv]; seq_start, max_len, slot as for causal_conv."""
+    state_in, state_out: float32 [slots, heads, dk, dv]; seq_start, max_len, slot as for causal_conv; max_len=1 for
+    packed single tokens, which a bound of 16 or more (as without it) sends through the prompts' kernel."""
     (_calls or _bind_calls()).gated_delta(
         q, k, v, dt, a, b, y, dt_bias, softplus, sigmoid, normalize, scale, seq_start, max_len, slot, state_in,
         state_out, stream)

@@ -209,9 +209,12 @@ __global__ void __launch_bounds__(128, LONG ? 3 : RK <= 8 ? 6 : 3) delta_row_ker
     }
 }
 
-// Longest sequence's rows from which prompts go in chunks.  Where blocks are few chunks are ahead from 6 rows on, where
-// they are many from 14.  Measured, us row by row and in chunks, heads of 128 x 128, bf16: 1 sequence of 32 heads, 4, 6, 8, 12
-// rows 5.0, 6.4, 7.4, 7.5 and 6.2; 64 of 8 heads 27, 34, 40, 54 and 68.
+// Longest sequence's rows from which prompts go in chunks.  Where blocks are few chunks are ahead from 10 rows or so on, where
+// they are many from 18; the rule asks for neither, nor how many sequences are as long as the longest.  Measured, us, heads of 128 x
+// 128, bf16, states in the L2: 1 sequence of 32 heads, 4, 8, 12, 15 rows 4.1, 5.6, 7.5, 8.7 row by row, 16 rows 6.5 in chunks; 64 of
+// 8 heads, 4, 8, 12, 15 rows 26, 37, 52, 61, 16 rows 69 in chunks.  A single token in a batch that goes in chunks costs a chunk's
+// time and an SM of its own: 127 of 32 heads and a prompt of 512 rows 560 us together, 99 and 38 as two calls; 128 with a loose
+// bound of their lengths 530, with a bound of 1 100.
 constexpr int kChunkedFrom = 16;
 // ... and from which the row kernel is the prompts': 64 sequences of 8 heads, 2, 4, 8 rows 21.4, 27.0, 40.2 us, as single
 // tokens 20.3, 28.2, 44.7.

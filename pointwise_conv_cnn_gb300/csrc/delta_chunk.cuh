@@ -157,18 +157,18 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool live)
 // parts, 22 bits, under a power of two for each column; products of second f16 parts, below 2^-22, are left out.  T and x are in three
 // bf16 parts for either type (products of parts below 2^-24 are left out): T holds e^(c_i - c_j), x the rows' values beside what the
 // state recalls, so that in a chunk where states grow or fall by much their numbers lie further apart than f16 reaches.
-// (In two f16 parts T was infinite from 65504 on, 23 rows of G = 0.5, and had lost what it says of a state 2^14 times as large
+// (In two f16 parts T was infinite from 65504 on, which 32 rows of G = 0.5 pass, and had lost what it says of a state 2^14 times as large
 // as the values; 503 us where these take 535.)  What only y needs has two bf16 parts, and y keeps 2^-9 or 2^-12 of itself:
 // S^T q is off by 2^-17 of its terms, P u, all four products of whose parts are taken, by 2^-16.
 //
-// 8192 rows of 32 heads of 128 x 128, bf16, 499 us: 1.95 us a chunk, 128 blocks on as many SMs.  A chunk's chain (S to its
-// parts, S^T k, x, u, S again) is what it costs: taken out alone, S^T k and q with the states' products save 103 us, the
-// inverse 53, the rows' loads 26, the products that make A and P 18.  The tensor cores are under a half busy, as are the issue
-// slots.  What was tried, us: four warps for 16 columns, 32 keys each, all factors in two f16 parts and keys converted in the block,
-// 1430, two warps so 1074 (the conversions bind); x and T in three bf16 parts 678 where 602 was; products in the order of
-// their sums, each waiting for the one before, 745 for 678; three slots of rows 731; S^T q's products after the meeting 503.
-// The loops are short because the roles' code has to stay in the instruction cache together: with the inverse's products
-// unrolled, and keys converted, the warps waited 2.6 cycles an instruction for their code.
+// 8192 rows of 32 heads of 128 x 128, bf16, 535 us: 2.1 us a chunk, 128 blocks on as many SMs; f16 624 us.  A chunk's chain (S to
+// its parts, S^T k, x, u, S again) is what it costs; with x and T in f16, 503 us in all, S^T k and q with the states' products taken
+// out alone saved 103 us, the inverse 53, the rows' loads 26, the products that make A and P 18.  The tensor cores are under a half
+// busy, as are the issue slots.  What was tried, us: four warps for 16 columns, 32 keys each, all factors in two f16 parts and keys
+// converted in the block, 1430, two warps so 1074 (the conversions bind); products in the order of their sums, each waiting for the
+// one before, 745 for 678; three slots of rows 731; S^T q's products after the meeting 503 for 499; T's parts stored one by one, as
+// rows, 581 for 552.  The loops are short because the roles' code has to stay in the instruction cache together: with the inverse's
+// products unrolled, and keys converted, the warps waited 2.6 cycles an instruction for their code.
 //
 // Four blocks make the same A, P and T, one for each 32 columns of a head.  A cluster that shares them would save some of
 // the 97 us above; its blocks would wait for each other in every chunk.
